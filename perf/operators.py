@@ -223,7 +223,8 @@ def _run_plain(s):
         return out
     x = s["x"].float()
     amax = x.abs().amax(dim=1, keepdim=True)
-    sx = torch.where(amax > 0, 127.0 / amax, torch.ones_like(amax))
+    # one rounded division (a scalar over a tensor would be a reciprocal and a product)
+    sx = torch.where(amax > 0, torch.full_like(amax, 127.0) / amax, torch.ones_like(amax))
     xq = torch.round(x * sx).clamp(-127, 127)
     if c["op"] == "linear":
         z = _plain_project(xq, sx, s["pw"], s["sw"], k, s.get("bw"))
