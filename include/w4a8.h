@@ -410,6 +410,110 @@ W4A8_API w4a8_status w4g_linear_q(const int8_t *Xq, int M, int K, int ldq, const
                          const uint8_t *Wp, int ldp, const float *sa, const int32_t *zp, int N,
                          const float *bias, unsigned flags, void *Y, int ldy, void *stream);
 
+/*
+ * MLP operators - the product with the rest of a feed-forward block's work in
+ * its epilogue, the gated feed-forward product, and the input gradients of
+ * both through the frozen codes. Steps 1-6 of "How it works" decide the
+ * integers exactly as in w4a8_linear; what follows is defined in real numbers
+ * and computed in float32:
+ *   linear      z = acc / (sx sw) + bias,   y = act(z) + residual
+ *   gated       g, u = two such z of one input, h = act(g) u
+ *   gradients   dz = dy act'(z);  dg = dh u act'(g), du = dh act(g);
+ *               dx[m][k] = sum_n dz[m][n] q[n][k] / sw[n] (over both
+ *               projections for the gated form): the straight-through
+ *               gradient of the row quantization, whose abs-max scale never
+ *               clips;  dbias[n] = sum_m dz[m][n].
+ *   act         none z; ReLU; SiLU z s(z), s the logistic function; GELU
+ *               z Phi(z); tanh GELU z s(2t), t = sqrt(2/pi)(z + 0.044715 z^3)
+ *               (the same as z (1 + tanh t) / 2). ReLU' at 0 is 0.
+ * The weights are symmetric per-channel INT4 as from w4_quantize_pack. The
+ * pages name none of these operators.
+ *
+ * Rows (X, residual, outputs, saved pre-activations, gradients) are all
+ * float32, or all bfloat16 with W4A8_IO_BF16; strides count elements and each
+ * row type needs its natural alignment only (16-byte aligned rows are
+ * faster). Biases, their gradients and scales are float32. Inputs must be
+ * finite. A bfloat16 output is rounded once, from float32. In the gradients
+ * each dz / sw is rounded to FP16 relative to a power of two of its row
+ * (2^-11 of the value) for bfloat16 rows, and held in two FP16 terms (2^-22)
+ * for float32 rows; sums are float32.
+ *
+ * 1 <= K <= W4A8_ACT_MAX_K. flags: W4A8_IO_* | W4A8_STATIC_WEIGHTS | one
+ * W4A8_PATH_*: AUTO, GENERIC, and where listed DECODE or TC (forced, for
+ * tests; W4A8_ERR_UNSUPPORTED where the form does not exist). Outputs must not
+ * overlap inputs, except that Y may be the residual itself (same pointer and
+ * stride). M == 0 enqueues nothing but the zeros of the bias gradients.
+ */
+#define W4A8_ACT_NONE      0
+#define W4A8_ACT_RELU      1
+#define W4A8_ACT_SILU      2
+#define W4A8_ACT_GELU      3
+#define W4A8_ACT_GELU_TANH 4
+#define W4A8_IO_F32        0x000u
+#define W4A8_IO_BF16       0x100u
+
+/* Largest K of these calls (the widened nibbles 16 q keep the INT32 sum exact). */
+#define W4A8_ACT_MAX_K 131072
+
+/* Workspace bytes of the forward calls: M rows, K inputs, N outputs per
+ * projection, projections 1 (w4a8_linear_act) or 2 (w4a8_glu), flags as for
+ * the call (the W4A8_IO_* type counts). 0 for arguments the call rejects. */
+W4A8_API size_t w4a8_act_workspace_size(int M, int K, int N, int projections, unsigned flags);
+
+/* Workspace bytes of the gradient calls, the same way; enough with and
+ * without bias gradients. */
+W4A8_API size_t w4a8_grad_workspace_size(int M, int K, int N, int projections, unsigned flags);
+
+/*
+ * w4a8_linear_act - quantize the rows of X, multiply, and finish with bias,
+ * activation and residual in the product's epilogue.
+ *   X [M][ldx], Wp/ldp/sw/bias as for w4a8_linear; act one W4A8_ACT_*.
+ *   R [M][ldr] residual, or NULL.   Y [M][ldy] out.
+ *   Z [M][ldz] out, or NULL: the pre-activations z for the gradient call.
+ *   workspace: at least w4a8_act_workspace_size bytes, 16-byte aligned.
+ */
+W4A8_API w4a8_status w4a8_linear_act(const void *X, int M, int K, int ldx,
+                                     const uint8_t *Wp, int ldp, const float *sw, int N,
+                                     const float *bias, int act, const void *R, int ldr, unsigned flags,
+                                     void *Y, int ldy, void *Z, int ldz,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * w4a8_glu - the gated feed-forward product H = act(X Wg + bg) * (X Wu + bu),
+ * both projections, the activation and the product in one kernel.
+ *   Wg, Wu [N][ldp] packed codes (one stride), sg, su [N] scales, bg, bu [N]
+ *   biases or NULL each.   H [M][ldh] out.
+ *   G, U [M][ldgu] out, both or neither: the pre-activations for w4a8_glu_grad.
+ */
+W4A8_API w4a8_status w4a8_glu(const void *X, int M, int K, int ldx,
+                              const uint8_t *Wg, const float *sg, const uint8_t *Wu, const float *su, int ldp,
+                              int N, const float *bg, const float *bu, int act, unsigned flags,
+                              void *H, int ldh, void *G, void *U, int ldgu,
+                              void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * w4a8_linear_act_grad - gradients of w4a8_linear_act towards X and the bias
+ * (the residual's is dY itself).
+ *   dY [M][lddy]; Z [M][ldz] as saved (ignored, and may be NULL, for
+ *   W4A8_ACT_NONE); Wp/ldp/sw as in the forward call.
+ *   dX [M][lddx] out, M rows of K.   dbias [N] float32 out, or NULL.
+ * Results repeat bit for bit from call to call.
+ */
+W4A8_API w4a8_status w4a8_linear_act_grad(const void *dY, int M, int N, int lddy, const void *Z, int ldz,
+                                          const uint8_t *Wp, int ldp, const float *sw, int K, int act,
+                                          unsigned flags, void *dX, int lddx, float *dbias,
+                                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * w4a8_glu_grad - gradients of w4a8_glu towards X and the biases.
+ *   dH [M][lddh]; G, U [M][ldgu] as saved.
+ *   dX [M][lddx] out, M rows of K.   dbg, dbu [N] float32 out, or NULL each.
+ */
+W4A8_API w4a8_status w4a8_glu_grad(const void *dH, int M, int N, int lddh, const void *G, const void *U, int ldgu,
+                                   const uint8_t *Wg, const float *sg, const uint8_t *Wu, const float *su, int ldp,
+                                   int K, int act, unsigned flags, void *dX, int lddx, float *dbg, float *dbu,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
 /* Which kernel path (W4A8_PATH_GENERIC / _DECODE / _TC) the calling thread's
  * last successful w4a8_linear / w4a8_linear_q / w8a8_linear / w8a8_linear_q
  * call enqueued (grouped calls: _DECODE); 0 if none. */

@@ -21,6 +21,8 @@
 #include "gemm_tc_grp.cuh"
 #include "gemm_tc_pair.cuh"
 #include "quant_pack_panel.cuh"
+#include "mlp_act.cuh"
+#include "mlp_simt.cuh"
 
 namespace w4a8 {
 namespace {
@@ -1208,3 +1210,5 @@ const char *w4a8_status_string(w4a8_status s) {
 }
 
 }  // extern "C"
+
+#include "mlp_abi.cuh"

@@ -24,12 +24,17 @@ PATH_AUTO, PATH_GENERIC, PATH_DECODE, PATH_TC = 0x00, 0x10, 0x20, 0x30
 PATH_DECODE_RING, PATH_DECODE_REGS, PATH_DECODE_SPLIT = 0x40, 0x50, 0x60
 PATH_TC_PAIR = 0x70
 MAX_K = 2097152
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
+IO_F32, IO_BF16 = 0x000, 0x100
+ACT_MAX_K = 131072
 
 _OUT = {"f32": OUT_F32, "bf16": OUT_BF16, "s32": OUT_S32}
 _OUT_DTYPE = {"f32": torch.float32, "bf16": torch.bfloat16, "s32": torch.int32}
 _PATH = {"auto": PATH_AUTO, "generic": PATH_GENERIC, "decode": PATH_DECODE, "tc": PATH_TC,
          "ring": PATH_DECODE_RING, "regs": PATH_DECODE_REGS, "split": PATH_DECODE_SPLIT,
          "tc2": PATH_TC_PAIR}
+_ACT = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH}
+_IO = {torch.float32: IO_F32, torch.bfloat16: IO_BF16}
 PATH_NAMES = {v: k for k, v in _PATH.items()}
 
 class Problem(ctypes.Structure):
@@ -66,6 +71,12 @@ SIGNATURES = {
     "w4g_quantize_pack": (_I, [_P, _I, _I, _I, _P, _I, _P, _P, _P]),
     "w4g_linear": (_I, [_P, _I, _I, _I, _P, _I, _P, _P, _I, _P, _U, _P, _I, _P, _S, _P]),
     "w4g_linear_q": (_I, [_P, _I, _I, _I, _P, _P, _I, _P, _P, _I, _P, _U, _P, _I, _P]),
+    "w4a8_act_workspace_size": (_S, [_I, _I, _I, _I, _U]),
+    "w4a8_grad_workspace_size": (_S, [_I, _I, _I, _I, _U]),
+    "w4a8_linear_act": (_I, [_P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, _U, _P, _I, _P, _I, _P, _S, _P]),
+    "w4a8_glu": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _P, _P, _I, _U, _P, _I, _P, _P, _I, _P, _S, _P]),
+    "w4a8_linear_act_grad": (_I, [_P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _I, _U, _P, _I, _P, _P, _S, _P]),
+    "w4a8_glu_grad": (_I, [_P, _I, _I, _I, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _U, _P, _I, _P, _P, _P, _S, _P]),
     "w4a8_last_path": (_U, []),
     "w4a8_last_launch_count": (_U, []),
     "w4a8_last_kernel": (ctypes.c_char_p, []),
@@ -462,6 +473,174 @@ def w4g_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor, s
                             flags_for(relu, out, path, static_weights), _ptr(y), ldy, _stream(stream)),
            "w4g_linear_q")
     return y
+
+
+# ------------------------------------------------------- MLP operators ---
+# The W4A8 product with bias, activation and residual in its epilogue, the
+# gated feed-forward product, and the input gradients of both. Rows are all
+# float32 or all bfloat16; act is "none", "relu", "silu", "gelu" or
+# "gelu_tanh". Formulas and rules: include/w4a8.h.
+
+def _io_flags(rows: torch.Tensor, act: str, path: str, static_weights: bool):
+    """(flags, activation code) of a call on rows of this type."""
+    if rows.dtype not in _IO:
+        raise ValueError("rows must be float32 or bfloat16")
+    if act not in _ACT:
+        raise ValueError(f"act must be one of {', '.join(_ACT)}")
+    return _IO[rows.dtype] | _PATH[path] | (STATIC_WEIGHTS if static_weights else 0), _ACT[act]
+
+
+def _io_rows(t: torch.Tensor | None, name: str, like: torch.Tensor, m: int, n: int) -> int:
+    """Row stride of an [m][n] tensor of like's dtype and device (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != like.dtype or t.device != like.device or tuple(t.shape) != (m, n):
+        raise ValueError(f"{name} must be a [{m}][{n}] {like.dtype} tensor on {like.device}")
+    return _row_stride(t, name)
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    # torch gives no meaning to the stride of a single row or column
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _weights(k: int, like: torch.Tensor, **named):
+    """Checks packed codes [N][ldp >= packed_ld(k)] and float32 vectors [N]; returns (N, ldp)."""
+    n = ldp = None
+    for name, t in named.items():
+        if t is None:
+            continue
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}")
+        if t.dtype == torch.uint8:
+            if t.dim() != 2 or t.shape[1] < packed_ld(k):
+                raise ValueError(f"{name} must be [N][>= {packed_ld(k)}] packed codes for K = {k}")
+            ld = _row_stride(t, name)
+            if ldp is not None and (ld != ldp or t.shape[0] != n):
+                raise ValueError("the two projections must have the same shape and row stride")
+            n, ldp = t.shape[0], ld
+        elif t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"{name} must be a contiguous float32 tensor of {n} values")
+    if n is None:
+        raise ValueError("packed codes must be uint8")
+    return n, ldp
+
+
+def _space(workspace, need: int, like: torch.Tensor):
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
+    elif workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {like.device}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def act_workspace_size(m: int, k: int, n: int, projections: int = 1, dtype=torch.float32) -> int:
+    return lib.w4a8_act_workspace_size(m, k, n, projections, _IO[dtype])
+
+
+def grad_workspace_size(m: int, k: int, n: int, projections: int = 1, dtype=torch.float32) -> int:
+    return lib.w4a8_grad_workspace_size(m, k, n, projections, _IO[dtype])
+
+
+def w4a8_linear_act(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, bias: torch.Tensor | None = None,
+                    act: str = "none", residual: torch.Tensor | None = None, save: bool = False,
+                    path: str = "auto", y: torch.Tensor | None = None, z: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None, static_weights: bool = False):
+    """Y[M][N] = act(dequant(quant8(X) @ unpack(Wp)^T) + bias) + residual, of
+    X's dtype. With save (or z given) returns (Y, Z), Z the pre-activations
+    that w4a8_linear_act_grad reads. y may be the residual itself."""
+    flags, fn = _io_flags(x, act, path, static_weights)
+    ldx = _row_stride(x, "X")
+    m, k = x.shape
+    n, ldp = _weights(k, x, wp=wp, sw=sw, bias=bias)
+    y = torch.empty((m, n), dtype=x.dtype, device=x.device) if y is None else y
+    z = torch.empty((m, n), dtype=x.dtype, device=x.device) if save and z is None else z
+    ldy, ldz, ldr = (_io_rows(t, nm, x, m, n) for t, nm in ((y, "Y"), (z, "Z"), (residual, "residual")))
+    with torch.cuda.device(x.device):
+        ws, wsb = _space(workspace, act_workspace_size(m, k, n, 1, x.dtype), x)
+        _check(lib.w4a8_linear_act(_ptr(x), m, k, ldx, _ptr(wp), ldp, _ptr(sw), n, _ptr(bias), fn,
+                                   _ptr(residual), ldr, flags, _ptr(y), ldy, _ptr(z), ldz, _ptr(ws), wsb,
+                                   _stream(stream)), "w4a8_linear_act")
+    return y if z is None else (y, z)
+
+
+def w4a8_glu(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, wu: torch.Tensor, su: torch.Tensor,
+             gate_bias: torch.Tensor | None = None, up_bias: torch.Tensor | None = None, act: str = "silu",
+             save: bool = False, path: str = "auto", h: torch.Tensor | None = None,
+             g: torch.Tensor | None = None, u: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None, stream=None, static_weights: bool = False):
+    """H[M][N] = act(G) * U of X's dtype, G and U the gate and up projections
+    of X with their biases. With save (or g and u given) returns (H, G, U) for
+    w4a8_glu_grad."""
+    flags, fn = _io_flags(x, act, path, static_weights)
+    ldx = _row_stride(x, "X")
+    m, k = x.shape
+    n, ldp = _weights(k, x, wg=wg, wu=wu, sg=sg, su=su, gate_bias=gate_bias, up_bias=up_bias)
+    h = torch.empty((m, n), dtype=x.dtype, device=x.device) if h is None else h
+    if save and g is None and u is None:
+        g, u = (torch.empty((m, n), dtype=x.dtype, device=x.device) for _ in range(2))
+    ldh, ldg, ldu = (_io_rows(t, nm, x, m, n) for t, nm in ((h, "H"), (g, "G"), (u, "U")))
+    if ldg != ldu:
+        raise ValueError("G and U must both be given, with one row stride")
+    with torch.cuda.device(x.device):
+        ws, wsb = _space(workspace, act_workspace_size(m, k, n, 2, x.dtype), x)
+        _check(lib.w4a8_glu(_ptr(x), m, k, ldx, _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su), ldp, n, _ptr(gate_bias),
+                            _ptr(up_bias), fn, flags, _ptr(h), ldh, _ptr(g), _ptr(u), ldg, _ptr(ws), wsb,
+                            _stream(stream)), "w4a8_glu")
+    return h if g is None else (h, g, u)
+
+
+def w4a8_linear_act_grad(dy: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, k: int, act: str = "none",
+                         z: torch.Tensor | None = None, bias_grad: bool = False, path: str = "auto",
+                         dx: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None,
+                         static_weights: bool = False):
+    """dX[M][k] (and with bias_grad dbias[N]) of w4a8_linear_act, of dY's
+    dtype; z is the saved pre-activations (not needed without activation).
+    The residual's gradient is dY."""
+    flags, fn = _io_flags(dy, act, path, static_weights)
+    lddy = _row_stride(dy, "dY")
+    m = dy.shape[0]
+    n, ldp = _weights(k, dy, wp=wp, sw=sw)
+    if dy.shape[1] != n:
+        raise ValueError(f"dY must have {n} columns")
+    if act == "none":
+        z = None
+    dx = torch.empty((m, k), dtype=dy.dtype, device=dy.device) if dx is None else dx
+    ldz, lddx = _io_rows(z, "Z", dy, m, n), _io_rows(dx, "dX", dy, m, k)
+    db = torch.empty(n, dtype=torch.float32, device=dy.device) if bias_grad else None
+    with torch.cuda.device(dy.device):
+        ws, wsb = _space(workspace, grad_workspace_size(m, k, n, 1, dy.dtype), dy)
+        _check(lib.w4a8_linear_act_grad(_ptr(dy), m, n, lddy, _ptr(z), ldz, _ptr(wp), ldp, _ptr(sw), k, fn,
+                                        flags, _ptr(dx), lddx, _ptr(db), _ptr(ws), wsb, _stream(stream)),
+               "w4a8_linear_act_grad")
+    return (dx, db) if bias_grad else dx
+
+
+def w4a8_glu_grad(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor,
+                  wu: torch.Tensor, su: torch.Tensor, k: int, act: str = "silu", bias_grad: bool = False,
+                  path: str = "auto", dx: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                  stream=None, static_weights: bool = False):
+    """dX[M][k] (and with bias_grad the two bias gradients [N]) of w4a8_glu,
+    of dH's dtype, from the saved G and U."""
+    flags, fn = _io_flags(dh, act, path, static_weights)
+    lddh = _row_stride(dh, "dH")
+    m = dh.shape[0]
+    n, ldp = _weights(k, dh, wg=wg, wu=wu, sg=sg, su=su)
+    if dh.shape[1] != n:
+        raise ValueError(f"dH must have {n} columns")
+    dx = torch.empty((m, k), dtype=dh.dtype, device=dh.device) if dx is None else dx
+    ldg, ldu, lddx = _io_rows(g, "G", dh, m, n), _io_rows(u, "U", dh, m, n), _io_rows(dx, "dX", dh, m, k)
+    if ldg != ldu:
+        raise ValueError("G and U must both be given, with one row stride")
+    dbg, dbu = (torch.empty(n, dtype=torch.float32, device=dh.device) if bias_grad else None for _ in range(2))
+    with torch.cuda.device(dh.device):
+        ws, wsb = _space(workspace, grad_workspace_size(m, k, n, 2, dh.dtype), dh)
+        _check(lib.w4a8_glu_grad(_ptr(dh), m, n, lddh, _ptr(g), _ptr(u), ldg, _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su),
+                                 ldp, k, fn, flags, _ptr(dx), lddx, _ptr(dbg), _ptr(dbu), _ptr(ws), wsb,
+                                 _stream(stream)), "w4a8_glu_grad")
+    return (dx, dbg, dbu) if bias_grad else dx
 
 
 def last_path() -> str:
