@@ -3,6 +3,8 @@
 // Included at the end of w4a8_abi.cu, whose helpers it uses.
 #pragma once
 
+#include "mlp_gemm.cuh"
+
 namespace w4a8 {
 namespace {
 
@@ -61,13 +63,33 @@ w4a8_status launch_quant_rows(const void *X, int M, int K, int ldx, const Worksp
     return from_cuda(e);
 }
 
+// The kernel path of a call: the forced one, else by size. A few thousand
+// products per SM do not fill a tensor-core tile's pipeline.
+unsigned mlp_path(int M, int K, int N, int segs, unsigned flags) {
+    const unsigned forced = flags & W4A8_PATH_MASK;
+    if (forced) return forced;
+    return (double)M * N * K * segs < 65536.0 ? W4A8_PATH_GENERIC : W4A8_PATH_TC;
+}
+
 template <bool GLU, typename T>
 w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a, const mlp::Proj &b, int ldp, int N,
                         int act, const mlp::EpiArgs &ea, unsigned flags, const Workspace &ws, cudaStream_t s) {
-    const unsigned path = flags & W4A8_PATH_MASK;
-    if (path != W4A8_PATH_AUTO && path != W4A8_PATH_GENERIC) return W4A8_ERR_UNSUPPORTED;
+    const unsigned path = mlp_path(M, K, N, GLU ? 2 : 1, flags);
+    if (path != W4A8_PATH_GENERIC && path != W4A8_PATH_TC) return W4A8_ERR_UNSUPPORTED;
+    if (path == W4A8_PATH_TC && tc::encode_fn() == nullptr) return W4A8_ERR_UNSUPPORTED;
     w4a8_status st = launch_quant_rows<T>(X, M, K, ldx, ws, flags, s);
     if (st != W4A8_OK) return st;
+    if (path == W4A8_PATH_TC) {
+        const mlp::PairArgs p = {M, N, (K + 127) / 128, 0, ws.sx, a, b, ea, act, 0,
+                                 (flags & W4A8_STATIC_WEIGHTS) != 0};
+        const mlp::PairCall c = {a.Wp, b.Wp, N, ldp, ws.xq, M, ws.ldq, device_info().sm_count};
+        st = mlp::launch_pair_any<GLU ? mlp::FWD_GLU : mlp::FWD_LINEAR, T>(p, c, s);
+        if (st != W4A8_OK) return st;
+        t_last_path = W4A8_PATH_TC;
+        t_last_launches = 2;
+        t_last_kernel = "k_mlp_pair";
+        return W4A8_OK;
+    }
     st = by_act(act, [&](auto A) {
         const dim3 grid((N + 127) / 128, M < 65535 ? M : 65535);
         return from_cuda(launch_pdl(mlp::k_mlp_simt<GLU, decltype(A)::value, T>, grid, dim3(128), 0, s, ws.xq, M, K,
@@ -128,9 +150,10 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
                      cudaStream_t s) {
     constexpr int SEGS = GLU ? 2 : 1;
     constexpr bool LO = std::is_same<T, float>::value;
-    const unsigned path = flags & W4A8_PATH_MASK;
-    if (path != W4A8_PATH_AUTO && path != W4A8_PATH_GENERIC) return W4A8_ERR_UNSUPPORTED;
     const int N = in.N;
+    const unsigned path = mlp_path(M, K, N, SEGS, flags);
+    if (path != W4A8_PATH_GENERIC && path != W4A8_PATH_TC) return W4A8_ERR_UNSUPPORTED;
+    if (path == W4A8_PATH_TC && tc::encode_fn() == nullptr) return W4A8_ERR_UNSUPPORTED;
     unsigned launches = 0;
     w4a8_status st = by_act(act, [&](auto A) {
         constexpr int ACT = decltype(A)::value;
@@ -149,6 +172,19 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
                                     dim3(mlp::GR_THREADS), 0, s, in, M, ws.seg, ws.P, ws.rs));
     });
     if (st != W4A8_OK) return st;
+    if (path == W4A8_PATH_TC) {
+        const int seg_stages = ws.seg / 64;
+        const mlp::PairArgs p = {M, K, SEGS * seg_stages, seg_stages, ws.rs, {}, {},
+                                 {nullptr, dX, nullptr, nullptr, 0, lddx, 0}, 0, 0,
+                                 (flags & W4A8_STATIC_WEIGHTS) != 0};
+        const mlp::PairCall c = {Wa, Wb, N, ldp, ws.P, ws.planes * M, SEGS * ws.seg, device_info().sm_count};
+        st = mlp::launch_pair_any<LO ? mlp::BWD_TWO : mlp::BWD_ONE, T>(p, c, s);
+        if (st != W4A8_OK) return st;
+        t_last_path = W4A8_PATH_TC;
+        t_last_launches = launches + 2;
+        t_last_kernel = "k_mlp_pair";
+        return W4A8_OK;
+    }
     const dim3 grid(((K + 7) / 8 + 127) / 128, M < 65535 ? M : 65535);
     cudaError_t e = launch_pdl(mlp::k_grad_simt<T>, grid, dim3(128), 0, s, (const __half *)ws.P, (const float *)ws.rs,
                                M, N, ws.seg, SEGS, ws.planes, Wa, Wb, ldp, K, static_cast<T *>(dX), lddx);

@@ -1,0 +1,606 @@
+// Tensor-core form of the MLP operators: a CTA pair (tcgen05.mma cta_group::2)
+// computes tiles of 256 weight-side rows x NT tokens with both operands in
+// shared memory. One kernel serves both directions:
+//
+//  forward   D[channel][token] = sum_k 16 q[n][k] xq[m][k], kind::i8, INT32.
+//            A: widened codes, k-major; B: the INT8 rows, k-major.
+//            Epilogue: dequantize, bias, activation, residual; or for the
+//            gated form both projections of a channel meet in registers.
+//  gradient  D[k][token] = sum_n q[n][k] P[m][n], kind::f16, float32.
+//            A: the codes in FP16, MN-major: a packed row holds one n and
+//            runs along k, which is D's row axis, so the one stored copy of
+//            the weights serves both directions without a transpose; B: the
+//            scaled FP16 gradient rows (k_grad_rows), n-major. For float32
+//            rows a second B tile holds the low parts and shares the
+//            widened weights.
+//
+// Bound: the tensor pipe at many tokens, the packed weights' stream at few.
+//
+// Why both operands sit in shared memory. With the widened weights in TMEM
+// the accumulators and the weight slots share its 512 columns, which caps the
+// tile at 160 tokens, and the stores into TMEM slow the MMAs down. Here two
+// 256-column accumulators fill TMEM, an MMA is 128 tensor cycles long, and per
+// SM and 128 cycles the pair moves 20 KB (forward; 18 KB gradient) through
+// shared memory: A and B reads of 4 KB each, 4 KB of B arriving, 2 KB (1 KB) of
+// packed weights in and out, 4 KB of widened weights written.
+//
+// Per CTA: 128 rows of A and half of the tile's tokens. Two rings: RAW stages
+// (packed weights and B, by TMA) and A slots (widened weights). Warp 0 loads,
+// warp 1 issues the MMAs (in the leader), warps 4-11 widen, warps 12-15 run
+// the epilogue of one tile while the next one's MMAs run (two accumulators).
+// No load is multicast. Every wait is bounded, as in gemm_tc_pair.cuh, whose
+// pair protocol this follows.
+//
+// Gated rows. The 32 TMEM lanes of an epilogue warp hold 16 gate and the same
+// 16 up channels (the widening warps place the rows so), and one shuffle per
+// two outputs brings a channel's pair together: lanes 0-15 finish the chunk's
+// first 16 tokens, lanes 16-31 the others.
+#pragma once
+
+#include "gemm_tc_pair.cuh"
+#include "mlp_act.cuh"
+#include "mlp_simt.cuh"
+
+namespace w4a8 {
+namespace mlp {
+
+enum { FWD_LINEAR = 0, FWD_GLU = 1, BWD_ONE = 2, BWD_TWO = 3 };  // BWD_TWO: two planes of B (float32 rows)
+
+constexpr int ROWS_CTA = 128;              // A rows per CTA
+constexpr int A_BYTES = ROWS_CTA * 128;    // a widened slot: 128 rows x 128 k INT8, or 128 k x 64 n FP16
+constexpr int EPI_SMEM = 32768;            // output staging
+constexpr int CONV_WARPS = 8;
+constexpr int FIRST_CONV = 4, FIRST_EPI = FIRST_CONV + CONV_WARPS;
+constexpr int PAIR_THREADS = 32 * (FIRST_EPI + 4);
+
+template <int MODE, int NT>
+struct Shape {
+    static constexpr bool FWD = MODE == FWD_LINEAR || MODE == FWD_GLU;
+    static constexpr int PLANES = MODE == BWD_TWO ? 2 : 1;
+    static constexpr int STEP = FWD ? 128 : 64;                 // contraction per stage
+    static constexpr int PACKED = FWD ? 128 * 64 : 64 * 64;     // packed bytes per stage
+    static constexpr int B_PLANE = NT / 2 * 128;
+    static constexpr int B_BYTES = PLANES * B_PLANE;
+    static constexpr int A_SLOTS = NT == 256 ? (MODE == BWD_TWO ? 2 : 3) : 4;
+    static constexpr int TABLES = 3072;                         // barriers and token tables
+    static constexpr int FIT = (232448 - 1024 - EPI_SMEM - TABLES - A_SLOTS * A_BYTES) / (PACKED + B_BYTES);
+    static constexpr int RAW = FIT < 8 ? FIT : 8;
+    static_assert(RAW >= A_SLOTS, "A-slot reuse waits on a stage barrier");
+};
+
+template <int MODE, int NT>
+struct alignas(1024) PairSmem {
+    using S = Shape<MODE, NT>;
+    uint8_t b[S::RAW][S::B_BYTES];
+    uint8_t a[S::A_SLOTS][A_BYTES];
+    uint8_t packed[S::RAW][S::PACKED];
+    uint8_t epi[EPI_SMEM];
+    uint64_t full[S::RAW];        // this CTA's TMA landed
+    uint64_t empty[S::RAW];       // MMAs reading the stage finished (both CTAs)
+    uint64_t ready[S::A_SLOTS];   // leader: both CTAs' slots widened (16 warps)
+    uint64_t acc_full[2];         // accumulator ready (both CTAs)
+    uint64_t acc_empty[2];        // leader: both CTAs' epilogues drained (8 warps)
+    uint64_t done;                // every MMA finished (both CTAs)
+    float tok[NT];                // 1/sx (forward) or the row's power of two
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct PairArgs {
+    int M;              // tokens
+    int N;              // rows of D: channels per projection, or K of the gradient
+    int stages;         // contraction stages per tile
+    int seg_stages;     // gradient: stages per segment
+    const float *tok;   // sx, or the rows' powers of two
+    Proj a, b;
+    EpiArgs e;          // gradient: Y = dX
+    int act, tma_out, static_w;
+};
+
+// ---- the MMA with both operands in shared memory ----
+template <bool FWD>
+__device__ __forceinline__ void mma_ss2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    if constexpr (FWD)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+            "r"(accumulate)
+            : "memory");
+}
+
+// Instruction descriptor of kind::f16: D float32 (bits 4-5 = 1), A and B FP16
+// (0), A MN-major (bit 15), B k-major, N >> 3 and M >> 4 as for kind::i8.
+__host__ __device__ constexpr uint32_t idesc_f16_mn(int m, int n) {
+    return (1u << 4) | (1u << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Shared-memory descriptor of the MN-major FP16 operand in 128-byte swizzled
+// rows: a row is 64 elements along M for one n, eight rows (n) an atom of
+// 1024 bytes, the next 64 elements along M `block` bytes further.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t block) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((block >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__device__ __forceinline__ void bulk_wait_read_0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void sts128(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ptx::smem_addr(p)), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------- widening ---
+// Forward: A row r of this CTA (thread r, one of two halves of its 64 packed
+// bytes). The packed tile is a 64-byte swizzled box (16-byte chunk c of row s
+// at chunk c ^ ((s >> 1) & 3)); the slot is 128-byte swizzled. Nibbles stay in
+// the high half of their byte (16 q), in the order the INT8 rows are stored in.
+template <bool GLU>
+__device__ __forceinline__ void widen_fwd(const uint8_t *packed, uint8_t *slot, int tid) {
+    const int r = tid & 127, half = tid >> 7;
+    // gated: rows 32 w + 0..15 are gate channels 16 w + .., 32 w + 16..31 the same up channels
+    const int s = GLU ? ((r & 16) << 2) + ((r >> 5) << 4) + (r & 15) : r;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = 2 * half + i;
+        const uint4 v = ptx::lds128(packed + s * 64 + 16 * (c ^ ((s >> 1) & 3)));
+        uint8_t *row = slot + r * 128;
+        constexpr uint32_t H = 0xF0F0F0F0u;
+        sts128(row + 16 * ((2 * c) ^ (r & 7)), (v.x << 4) & H, v.x & H, (v.y << 4) & H, v.y & H);
+        sts128(row + 16 * ((2 * c + 1) ^ (r & 7)), (v.z << 4) & H, v.z & H, (v.w << 4) & H, v.w & H);
+    }
+}
+
+// Gradient: packed row n (one n, 128 k), 16-byte chunk c = 32 codes. Nibble u
+// of q + 8 is put under the FP16 exponent of 1024 (1024 + u, exact) and 1032
+// is subtracted. Masking words of eight codes gives them in the order
+// k0 k4 k1 k5 k2 k6 k3 k7, undone by the epilogue's row index.
+__device__ __forceinline__ void widen_bwd(const uint8_t *packed, uint8_t *slot, int tid) {
+    const int n = tid & 63, c = tid >> 6;
+    const uint4 v = ptx::lds128(packed + n * 64 + 16 * (c ^ ((n >> 1) & 3)));
+    const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+    uint8_t *row = slot + (c >> 1) * (64 * 128) + n * 128;
+    const __half2 off = __floats2half2_rn(1032.0f, 1032.0f);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t t = ((p[w] >> (4 * j)) & 0x000F000Fu) ^ 0x64086408u;
+            const __half2 h = __hsub2(*reinterpret_cast<__half2 *>(&t), off);
+            o[j] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        sts128(row + 16 * ((4 * (c & 1) + w) ^ (n & 7)), o[0], o[1], o[2], o[3]);
+    }
+}
+
+// ---------------------------------------------------------------- epilogue ---
+// One thread's values of a 32-token chunk: n is its output column, tokens
+// m0 + j. Staged (stg non-null): T tiles [32][COLS] for the TMA store;
+// direct: guarded stores to memory.
+template <typename T>
+struct Out {
+    T *stg;        // staging tile, or null
+    T *mem;        // row 0, column 0 of the array
+    int ld;
+    __device__ __forceinline__ void put(int tok, int col, int cols, int m, int n, bool ok, float v) const {
+        if (stg) st_elem(stg + tok * cols + col, v);
+        else if (ok) st_elem(mem + (size_t)m * ld + n, v);
+    }
+};
+
+template <int ACT, bool GLU, typename T>
+__device__ __forceinline__ void fwd_chunk(const uint32_t (&v)[32], const float *__restrict__ tok, float rsw, float b,
+                                          int lane, int col, int m0, int M, int n, bool n_ok, const Out<T> &y,
+                                          const Out<T> &z, const Out<T> &u, const T *R, int ldr) {
+    if constexpr (GLU) {
+        const bool gate = lane < 16;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float z0 = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[j]), tok[j]), rsw) + b;
+            const float z1 = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[16 + j]), tok[16 + j]), rsw) + b;
+            const float got = __shfl_xor_sync(0xffffffffu, gate ? z1 : z0, 16);
+            const float g = gate ? z0 : got, up = gate ? got : z1;
+            const int t = gate ? j : 16 + j;
+            const bool ok = n_ok && m0 + t < M;
+            y.put(t, col, 64, m0 + t, n, ok, act_value<ACT>(g) * up);
+            if (z.mem) {
+                z.put(t, col, 64, m0 + t, n, ok, g);
+                u.put(t, col, 64, m0 + t, n, ok, up);
+            }
+        }
+    } else {
+        float r[32];
+        if (R) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                r[j] = n_ok && m0 + j < M ? ld_elem(R + (size_t)(m0 + j) * ldr + n) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float zz = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[j]), tok[j]), rsw) + b;
+            float yy = act_value<ACT>(zz);
+            if (R) yy += r[j];
+            const bool ok = n_ok && m0 + j < M;
+            y.put(j, col, 128, m0 + j, n, ok, yy);
+            if (z.mem) z.put(j, col, 128, m0 + j, n, ok, zz);
+        }
+    }
+}
+
+template <int MODE, int NT, typename T>
+__global__ void __launch_bounds__(PAIR_THREADS, 1)
+k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CUtensorMap tm_wb,
+           const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
+           const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_u, const PairArgs p) {
+    using S = Shape<MODE, NT>;
+    constexpr bool FWD = S::FWD, GLU = MODE == FWD_GLU;
+    constexpr int RAW = S::RAW, A_SLOTS = S::A_SLOTS, HT = NT / 2;
+    constexpr int TILE_ROWS = GLU ? ROWS_CTA : 2 * ROWS_CTA;  // output columns per pair tile
+    extern __shared__ uint8_t smem_raw[];
+    auto &sm = *reinterpret_cast<PairSmem<MODE, NT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)ptx::cluster_ctarank();
+    const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
+    const int tiles_m = (p.M + NT - 1) / NT, tiles_n = (p.N + TILE_ROWS - 1) / TILE_ROWS;
+    const int num_tiles = tiles_m * tiles_n;
+    const int my_tiles = (num_tiles - pair + npairs - 1) / npairs;
+    const int total = my_tiles * p.stages;
+    volatile int *abort = &sm.abort;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < RAW; ++s) {
+            ptx::mbar_init(&sm.full[s], 1);
+            ptx::mbar_init(&sm.empty[s], 1);
+        }
+        for (int a = 0; a < A_SLOTS; ++a) ptx::mbar_init(&sm.ready[a], 2 * CONV_WARPS);
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&sm.acc_full[b], 1);
+            ptx::mbar_init(&sm.acc_empty[b], 8);
+        }
+        ptx::mbar_init(&sm.done, 1);
+        sm.abort = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tensormap(&tm_wa);
+        ptx::prefetch_tensormap(&tm_x);
+    }
+    if (warp == 1) {
+        tcp::tmem_alloc2(&sm.tmem_base, 512);
+        tcp::tmem_relinquish2();
+    }
+    ptx::tc_fence_before();
+    // both CTAs' barriers initialized and TMEM allocated before any remote use
+    ptx::cluster_arrive_release();
+    ptx::cluster_wait_acquire();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+
+    // Packed weights of stage st of a tile (its full barrier then also waits
+    // for the tokens' tile).
+    auto load_weights = [&](int slot, int n_tile, int st) {
+        ptx::mbar_arrive_expect_tx(&sm.full[slot], S::PACKED + S::B_BYTES);
+        if constexpr (MODE == FWD_LINEAR) {
+            ptx::tma_load_2d(sm.packed[slot], &tm_wa, 64 * st, n_tile * 256 + rank * 128, &sm.full[slot]);
+        } else if constexpr (GLU) {
+            const int n0 = n_tile * 128 + rank * 64;
+            ptx::tma_load_2d(sm.packed[slot], &tm_wa, 64 * st, n0, &sm.full[slot]);
+            ptx::tma_load_2d(sm.packed[slot] + 4096, &tm_wb, 64 * st, n0, &sm.full[slot]);
+        } else {
+            const bool second = st >= p.seg_stages;
+            ptx::tma_load_2d(sm.packed[slot], second ? &tm_wb : &tm_wa, n_tile * 128 + rank * 64,
+                             64 * (second ? st - p.seg_stages : st), &sm.full[slot]);
+        }
+    };
+    // Static weights: the first stages' packed tiles are requested before the
+    // dependency wait; the tokens are read only after it.
+    const int pre_w = p.static_w ? min(RAW, total) : 0;
+    if (warp == 0 && lane == 0)
+        for (int it = 0; it < pre_w; ++it)
+            load_weights(it, (pair + (it / p.stages) * npairs) / tiles_m, it % p.stages);
+    __syncwarp();
+    griddep_launch_dependents();
+    griddep_wait();
+
+    if (warp == 0) {
+        // ---------------------------------------------------- TMA producer (each CTA: its halves)
+        if (lane == 0) {
+            int slot = 0, it = 0;
+            uint32_t phase = 0, issued = 0, last_par = 0;
+            bool ok = true;
+            for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
+                const int n_tile = tile / tiles_m, m_tile = tile % tiles_m;
+                const int m0 = m_tile * NT + rank * HT;
+                for (int st = 0; st < p.stages; ++st, ++it) {
+                    if (it >= pre_w) {
+                        if (!ptx::mbar_wait(&sm.empty[slot], phase ^ 1, abort)) { ok = false; break; }
+                        load_weights(slot, n_tile, st);
+                    }
+#pragma unroll
+                    for (int pl = 0; pl < S::PLANES; ++pl)
+                        ptx::tma_load_2d(sm.b[slot] + pl * S::B_PLANE, &tm_x, S::STEP * st, pl * p.M + m0,
+                                         &sm.full[slot]);
+                    issued |= 1u << slot;
+                    last_par = (last_par & ~(1u << slot)) | (phase << slot);
+                    if (++slot == RAW) { slot = 0; phase ^= 1; }
+                }
+            }
+            // Drain: every load this thread issued lands before the CTA exits.
+            if (!ok)
+                for (int s = 0; s < RAW; ++s)
+                    if (issued & (1u << s)) ptx::mbar_wait_drain(&sm.full[s], (last_par >> s) & 1u);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------- MMA issuer (leader only)
+        // The widening warps of both CTAs arrive on ready only after their own
+        // wait on full[] of the same stage, so both CTAs' token halves have
+        // landed too once it flips.
+        if (rank == 0 && lane == 0) {
+            constexpr uint32_t idesc = FWD ? ptx::idesc_i8(256, NT) : idesc_f16_mn(256, NT);
+            int slot = 0, as = 0, st = 0, buf = 0;
+            uint32_t aphase = 0, bphase = 0;
+            bool ok = total > 0 ? ptx::mbar_wait(&sm.ready[0], 0, abort) : true;
+            for (int it = 0; it < total && ok; ++it) {
+                if (st == 0 && !ptx::mbar_wait(&sm.acc_empty[buf], bphase ^ 1u, abort)) break;
+                ptx::tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(buf * 256);
+                const uint32_t a = ptx::smem_addr(sm.a[as]), b = ptx::smem_addr(sm.b[slot]);
+                int nas = as + 1;
+                uint32_t naphase = aphase;
+                if (nas == A_SLOTS) { nas = 0; naphase ^= 1u; }
+                bool next_ok = true;
+#pragma unroll
+                for (int pl = 0; pl < S::PLANES; ++pl)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        // wait for the next operands while the queued MMAs run
+                        if (pl == S::PLANES - 1 && kk == 3 && it + 1 < total)
+                            next_ok = ptx::mbar_wait(&sm.ready[nas], naphase, abort);
+                        const uint64_t ad = FWD ? ptx::sdesc_k_sw128(a + 32 * kk) : sdesc_mn_sw128(a + 2048 * kk, 64 * 128);
+                        mma_ss2<FWD>(d, ad, ptx::sdesc_k_sw128(b + pl * S::B_PLANE + 32 * kk), idesc, (st | pl | kk) != 0);
+                    }
+                tcp::mma_commit2_both(&sm.empty[slot]);
+                if (++st == p.stages) {
+                    tcp::mma_commit2_both(&sm.acc_full[buf]);
+                    st = 0;
+                    if (++buf == 2) { buf = 0; bphase ^= 1u; }
+                }
+                if (++slot == RAW) slot = 0;
+                as = nas;
+                aphase = naphase;
+                ok = next_ok;
+            }
+            if (total > 0) tcp::mma_commit2_both(&sm.done);
+        }
+    } else if (warp >= FIRST_CONV && warp < FIRST_EPI) {
+        // ---------------------------------------------------- widening (each CTA: its 128 rows)
+        const int tid = threadIdx.x - 32 * FIRST_CONV;
+        int slot = 0, as = 0, old = 0;        // old: the stage slot of iteration it - A_SLOTS
+        uint32_t phase = 0, ophase = 0;
+        for (int it = 0; it < total; ++it) {
+            bool got = ptx::mbar_wait(&sm.full[slot], phase, abort);
+            // the A slot was last read by the MMAs of iteration it - A_SLOTS
+            if (it >= A_SLOTS) {
+                got = got && ptx::mbar_wait(&sm.empty[old], ophase, abort);
+                if (++old == RAW) { old = 0; ophase ^= 1u; }
+            }
+            if (!__all_sync(0xffffffffu, got)) break;
+            if constexpr (FWD) widen_fwd<GLU>(sm.packed[slot], sm.a[as], tid);
+            else widen_bwd(sm.packed[slot], sm.a[as], tid);
+            tcp::fence_proxy_async_smem();  // the slot's generic writes, before the MMA reads them
+            __syncwarp();
+            if (lane == 0) tcp::mbar_arrive_leader(&sm.ready[as]);
+            if (++slot == RAW) { slot = 0; phase ^= 1u; }
+            if (++as == A_SLOTS) as = 0;
+        }
+    } else if (warp >= FIRST_EPI) {
+        // ---------------------------------------------------- epilogue (each CTA: its 128 TMEM lanes)
+        const int q = warp & 3, et = threadIdx.x - 32 * FIRST_EPI;
+        constexpr int COLS = GLU ? 64 : 128;
+        // this thread's output column inside the CTA's COLS (the gradient's
+        // rows come in the order of the widening masks)
+        const int col = GLU ? 16 * q + (lane & 15)
+                            : FWD ? et : (et & ~7) | ((et & 7) >> 1) | ((et & 1) << 2);
+        const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        const int outs = 1 + (FWD && p.e.Z ? (GLU ? 2 : 1) : 0);
+        constexpr int STG = 32 * COLS;  // elements of a staging tile
+        const bool twice = 2 * outs * STG * (int)sizeof(T) <= EPI_SMEM;
+        int buf = 0, sb = 0;
+        uint32_t acc_phase = 0;
+        for (int tile = pair; tile < num_tiles; tile += npairs) {
+            const int n_tile = tile / tiles_m, m_base = (tile % tiles_m) * NT;
+            const int n_base = n_tile * TILE_ROWS + rank * COLS, n = n_base + col;
+            const bool n_ok = n < p.N;
+            for (int c = et; c < NT; c += 128) {
+                const float t = m_base + c < p.M ? ld_dep(p.tok + m_base + c) : 1.0f;
+                sm.tok[c] = FWD ? __frcp_rn(t) : t;
+            }
+            float rsw = 1.0f, b = 0.0f;
+            if constexpr (FWD) {
+                const bool up = GLU && lane >= 16;
+                const float *sw = up ? p.b.sw : p.a.sw, *bias = up ? p.b.bias : p.a.bias;
+                rsw = n_ok ? __frcp_rn(ld_dep(sw + n)) * 0.0625f : 1.0f;  // the accumulator holds 16 x the sum
+                b = n_ok && bias ? ld_dep(bias + n) : 0.0f;
+            }
+            // One decision for all four warps (this barrier also publishes the table).
+            if (!ptx::bar_and(1, 128, ptx::mbar_wait(&sm.acc_full[buf], acc_phase, abort))) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < NT; c0 += 32) {
+                const int m0 = m_base + c0;
+                if (m0 >= p.M) break;
+                uint32_t v[32];
+                ptx::tmem_ld_32x32b_x32(tmem + lane_base + (uint32_t)(buf * 256 + c0), v);
+                ptx::tmem_wait_ld();
+                if (p.tma_out) {
+                    // the staging tiles written below were last read by the
+                    // stores of the chunk before last (or the last one)
+                    if (et == 0) {
+                        if (twice) tcp::bulk_wait_read_1();
+                        else bulk_wait_read_0();
+                    }
+                    ptx::bar_sync(1, 128);
+                }
+                T *stg = p.tma_out ? reinterpret_cast<T *>(sm.epi) + (twice ? sb * outs * STG : 0) : nullptr;
+                const Out<T> y = {stg, static_cast<T *>(p.e.Y), p.e.ldy};
+                if constexpr (FWD) {
+                    const Out<T> z = {stg ? stg + STG : nullptr, static_cast<T *>(p.e.Z), p.e.ldz};
+                    const Out<T> u = {stg ? stg + 2 * STG : nullptr, static_cast<T *>(p.e.U), p.e.ldz};
+                    const T *R = static_cast<const T *>(p.e.R);
+#define W4A8_CHUNK(A) \
+    fwd_chunk<A, GLU, T>(v, sm.tok + c0, rsw, b, lane, col, m0, p.M, n, n_ok, y, z, u, R, p.e.ldr)
+                    switch (p.act) {
+                        case W4A8_ACT_NONE: W4A8_CHUNK(W4A8_ACT_NONE); break;
+                        case W4A8_ACT_RELU: W4A8_CHUNK(W4A8_ACT_RELU); break;
+                        case W4A8_ACT_SILU: W4A8_CHUNK(W4A8_ACT_SILU); break;
+                        case W4A8_ACT_GELU: W4A8_CHUNK(W4A8_ACT_GELU); break;
+                        default: W4A8_CHUNK(W4A8_ACT_GELU_TANH); break;
+                    }
+#undef W4A8_CHUNK
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        y.put(j, col, COLS, m0 + j, n, n_ok && m0 + j < p.M, __uint_as_float(v[j]) * sm.tok[c0 + j]);
+                }
+                if (p.tma_out) {
+                    tcp::fence_proxy_async_smem();  // the staging writes, before the store reads them
+                    ptx::bar_sync(1, 128);
+                    if (et == 0 && n_base < p.N) {
+                        tcp::tma_store_2d(&tm_y, stg, n_base, m0);
+                        if (outs > 1) tcp::tma_store_2d(&tm_z, stg + STG, n_base, m0);
+                        if (outs > 2) tcp::tma_store_2d(&tm_u, stg + 2 * STG, n_base, m0);
+                        tcp::bulk_commit_group();
+                    }
+                    sb ^= 1;
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tcp::mbar_arrive_leader(&sm.acc_empty[buf]);
+            if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+            ptx::bar_sync(1, 128);  // the table is rewritten next tile
+        }
+        // the output stores have completed before the CTA exits
+        if (et == 0 && p.tma_out) tcp::bulk_wait_all();
+    }
+
+    // Every MMA of the pair has finished before TMEM is released.
+    if (warp == 1) {
+        if (total > 0 && lane == 0) ptx::mbar_wait_drain(&sm.done, 0);
+        __syncwarp();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    // the pair meets before TMEM is released and before either CTA exits
+    ptx::cluster_arrive_release();
+    ptx::cluster_wait_acquire();
+    ptx::tc_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tcp::tmem_dealloc2(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------- host side ---
+
+// What a launch needs beside PairArgs: the operands' shapes.
+struct PairCall {
+    const uint8_t *Wa, *Wb;
+    int w_rows, ldp;             // packed rows and their stride
+    const void *X;               // INT8 rows [M][ldq], or FP16 rows [planes M][width]
+    int x_rows, x_inner;         // rows and row elements (= stride) of X
+    int sm_count;
+};
+
+template <int MODE, int NT, typename T>
+w4a8_status launch_pair(PairArgs p, const PairCall &c, cudaStream_t stream) {
+    using S = Shape<MODE, NT>;
+    constexpr bool GLU = MODE == FWD_GLU;
+    constexpr int COLS = GLU ? 64 : 128, TILE_ROWS = 2 * COLS;
+    auto kern = k_mlp_pair<MODE, NT, T>;
+    const int smem = (int)sizeof(PairSmem<MODE, NT>) + 1024;
+    if (!raise_smem_limit(reinterpret_cast<const void *>(kern), smem)) return W4A8_ERR_CUDA;
+    CUtensorMap wa, wb, x, out[3];
+    memset(out, 0, sizeof(out));
+    const uint32_t box_rows = S::FWD ? (GLU ? 64 : 128) : 64;
+    auto map_w = [&](CUtensorMap *m, const uint8_t *W) {
+        return tc::make_map_u8(m, W, (uint64_t)c.ldp, (uint64_t)c.w_rows, (uint64_t)c.ldp, 64, box_rows,
+                               CU_TENSOR_MAP_SWIZZLE_64B);
+    };
+    if (!map_w(&wa, c.Wa) || !map_w(&wb, c.Wb)) return W4A8_ERR_CUDA;
+    const size_t xsz = S::FWD ? 1 : 2;
+    if (!tc::make_map_2d(&x, S::FWD ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, c.X,
+                         (uint64_t)c.x_inner, (uint64_t)c.x_rows, (uint64_t)c.x_inner * xsz, 128 / xsz, NT / 2,
+                         CU_TENSOR_MAP_SWIZZLE_128B))
+        return W4A8_ERR_CUDA;
+    // Outputs go through tensor maps where every array's base, row stride and
+    // row of N outputs end on 16-byte boundaries (the store's bounds check on
+    // the inner dimension works in 16-byte units); directly otherwise.
+    void *const arr[3] = {p.e.Y, p.e.Z, p.e.U};
+    const int ld[3] = {p.e.ldy, p.e.ldz, p.e.ldz};
+    bool tma = (size_t)p.N * sizeof(T) % 16 == 0;
+    for (int i = 0; i < 3; ++i)
+        if (arr[i]) tma = tma && aligned16(arr[i]) && (size_t)ld[i] * sizeof(T) % 16 == 0;
+    const CUtensorMapDataType t = sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    for (int i = 0; i < 3 && tma; ++i)
+        if (arr[i])
+            tma = tc::make_map_2d(&out[i], t, arr[i], (uint64_t)p.N, (uint64_t)p.M, (uint64_t)ld[i] * sizeof(T), COLS,
+                                  32, CU_TENSOR_MAP_SWIZZLE_NONE);
+    p.tma_out = tma;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(PAIR_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const long long tiles = (long long)((p.M + NT - 1) / NT) * ((p.N + TILE_ROWS - 1) / TILE_ROWS);
+    const long long pairs = tiles < c.sm_count / 2 ? tiles : c.sm_count / 2;
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    return from_cuda(cudaLaunchKernelEx(&cfg, kern, wa, wb, x, out[0], out[1], out[2], p));
+}
+
+// Token tile: the one with the least rounds of tiles times the cost of a
+// stage, where an MMA stage takes 2 NT tensor cycles (twice for two planes)
+// and the widening about 400 whatever the tile.
+inline int pick_pair_tile(int M, int rows, int tile_rows, int planes, int sm_count) {
+    const int cand[3] = {256, 128, 64};
+    int best = 256;
+    long long best_cost = -1;
+    for (int nt : cand) {
+        const long long tiles = (long long)((M + nt - 1) / nt) * ((rows + tile_rows - 1) / tile_rows);
+        const long long rounds = (tiles + sm_count / 2 - 1) / (sm_count / 2);
+        const long long mma = 2LL * nt * planes;
+        const long long cost = rounds * (mma > 400 ? mma : 400);
+        if (best_cost < 0 || cost < best_cost) {
+            best_cost = cost;
+            best = nt;
+        }
+    }
+    return best;
+}
+
+template <int MODE, typename T>
+w4a8_status launch_pair_any(const PairArgs &p, const PairCall &c, cudaStream_t s) {
+    const int nt = pick_pair_tile(p.M, p.N, MODE == FWD_GLU ? 128 : 256, Shape<MODE, 64>::PLANES, c.sm_count);
+    if (nt == 256) return launch_pair<MODE, 256, T>(p, c, s);
+    if (nt == 128) return launch_pair<MODE, 128, T>(p, c, s);
+    return launch_pair<MODE, 64, T>(p, c, s);
+}
+
+}  // namespace mlp
+}  // namespace w4a8
