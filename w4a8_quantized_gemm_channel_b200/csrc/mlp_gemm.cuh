@@ -81,7 +81,7 @@ struct alignas(1024) PairSmem {
     uint64_t acc_full[2];         // accumulator ready (both CTAs)
     uint64_t acc_empty[2];        // leader: both CTAs' epilogues drained (8 warps)
     uint64_t done;                // every MMA finished (both CTAs)
-    float tok[NT];                // 1/sx (forward) or the row's power of two
+    alignas(16) float tok[NT];    // 1/sx (forward) or the row's power of two
     uint32_t tmem_base;
     int abort;
 };
@@ -184,56 +184,77 @@ __device__ __forceinline__ void widen_bwd(const uint8_t *packed, uint8_t *slot, 
 }
 
 // ---------------------------------------------------------------- epilogue ---
-// One thread's values of a 32-token chunk: n is its output column, tokens
-// m0 + j. Staged (stg non-null): T tiles [32][COLS] for the TMA store;
-// direct: guarded stores to memory.
-template <typename T>
-struct Out {
-    T *stg;        // staging tile, or null
-    T *mem;        // row 0, column 0 of the array
-    int ld;
-    __device__ __forceinline__ void put(int tok, int col, int cols, int m, int n, bool ok, float v) const {
-        if (stg) st_elem(stg + tok * cols + col, v);
-        else if (ok) st_elem(mem + (size_t)m * ld + n, v);
-    }
-};
+// Half a chunk (16 tokens) of one TMEM lane, written to the staging tiles
+// [32][COLS] of T at `st` (shared address of this thread's column in the
+// half's first row; the saved pre-activations' tiles follow `tile` bytes
+// apart). Every choice is a template argument: branches per element made this
+// loop several times slower.
+__device__ __forceinline__ void sts_elem(uint32_t a, float v, float) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void sts_elem(uint32_t a, float v, __nv_bfloat16) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v))) : "memory");
+}
 
-template <int ACT, bool GLU, typename T>
-__device__ __forceinline__ void fwd_chunk(const uint32_t (&v)[32], const float *__restrict__ tok, float rsw, float b,
-                                          int lane, int col, int m0, int M, int n, bool n_ok, const Out<T> &y,
-                                          const Out<T> &z, const Out<T> &u, const T *R, int ldr) {
-    if constexpr (GLU) {
-        const bool gate = lane < 16;
+template <int ACT, bool GLU, bool SAVE, bool RES, typename T>
+__device__ __forceinline__ void fwd_half(const uint32_t (&v)[16], const float (&r)[16], const float *tok, float rsw,
+                                         float b, int lane, uint32_t st, int tile) {
+    constexpr int ROW = (GLU ? 64 : 128) * (int)sizeof(T);
+    float z[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float z0 = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[j]), tok[j]), rsw) + b;
-            const float z1 = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[16 + j]), tok[16 + j]), rsw) + b;
-            const float got = __shfl_xor_sync(0xffffffffu, gate ? z1 : z0, 16);
-            const float g = gate ? z0 : got, up = gate ? got : z1;
-            const int t = gate ? j : 16 + j;
-            const bool ok = n_ok && m0 + t < M;
-            y.put(t, col, 64, m0 + t, n, ok, act_value<ACT>(g) * up);
-            if (z.mem) {
-                z.put(t, col, 64, m0 + t, n, ok, g);
-                u.put(t, col, 64, m0 + t, n, ok, up);
+    for (int i = 0; i < 4; ++i) {
+        const float4 t = reinterpret_cast<const float4 *>(tok)[i];
+        z[4 * i] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[4 * i]), t.x), rsw) + b;
+        z[4 * i + 1] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[4 * i + 1]), t.y), rsw) + b;
+        z[4 * i + 2] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[4 * i + 2]), t.z), rsw) + b;
+        z[4 * i + 3] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[4 * i + 3]), t.w), rsw) + b;
+    }
+    if constexpr (GLU) {
+        // lanes 0-15 finish tokens 0-7 of the half, lanes 16-31 tokens 8-15
+        const bool gate = lane < 16;
+        const uint32_t at = st + (gate ? 0 : 8 * ROW);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float got = __shfl_xor_sync(0xffffffffu, gate ? z[8 + j] : z[j], 16);
+            const float g = gate ? z[j] : got, u = gate ? got : z[8 + j];
+            sts_elem(at + j * ROW, act_value<ACT>(g) * u, T());
+            if constexpr (SAVE) {
+                sts_elem(at + j * ROW + tile, g, T());
+                sts_elem(at + j * ROW + 2 * tile, u, T());
             }
         }
     } else {
-        float r[32];
-        if (R) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-                r[j] = n_ok && m0 + j < M ? ld_elem(R + (size_t)(m0 + j) * ldr + n) : 0.0f;
+        for (int j = 0; j < 16; ++j) {
+            float y = act_value<ACT>(z[j]);
+            if constexpr (RES) y += r[j];
+            sts_elem(st + j * ROW, y, T());
+            if constexpr (SAVE) sts_elem(st + j * ROW + tile, z[j], T());
         }
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float zz = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[j]), tok[j]), rsw) + b;
-            float yy = act_value<ACT>(zz);
-            if (R) yy += r[j];
-            const bool ok = n_ok && m0 + j < M;
-            y.put(j, col, 128, m0 + j, n, ok, yy);
-            if (z.mem) z.put(j, col, 128, m0 + j, n, ok, zz);
-        }
+    }
+}
+
+template <int ACT, bool GLU, typename T>
+__device__ __forceinline__ void fwd_half_any(bool save, bool res, const uint32_t (&v)[16], const float (&r)[16],
+                                             const float *tok, float rsw, float b, int lane, uint32_t st, int tile) {
+    if (GLU || !res) {
+        if (save) fwd_half<ACT, GLU, true, false, T>(v, r, tok, rsw, b, lane, st, tile);
+        else fwd_half<ACT, GLU, false, false, T>(v, r, tok, rsw, b, lane, st, tile);
+    } else {
+        if (save) fwd_half<ACT, GLU, true, true, T>(v, r, tok, rsw, b, lane, st, tile);
+        else fwd_half<ACT, GLU, false, true, T>(v, r, tok, rsw, b, lane, st, tile);
+    }
+}
+
+// A staged chunk to memory by the four warps, where the arrays' alignment
+// does not allow the TMA store.
+template <int COLS, typename T>
+__device__ __forceinline__ void copy_out(const uint8_t *stg, void *out, int ld, int m0, int M, int n0, int N, int et) {
+    const T *s = reinterpret_cast<const T *>(stg);
+    const int rows = min(32, M - m0);
+    for (int i = et; i < rows * COLS; i += 128) {
+        const int r = i / COLS, c = i % COLS;
+        if (n0 + c < N) static_cast<T *>(out)[(size_t)(m0 + r) * ld + n0 + c] = s[i];
     }
 }
 
@@ -411,8 +432,9 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                             : FWD ? et : (et & ~7) | ((et & 7) >> 1) | ((et & 1) << 2);
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
         const int outs = 1 + (FWD && p.e.Z ? (GLU ? 2 : 1) : 0);
-        constexpr int STG = 32 * COLS;  // elements of a staging tile
-        const bool twice = 2 * outs * STG * (int)sizeof(T) <= EPI_SMEM;
+        constexpr int STG = 32 * COLS * (int)sizeof(T);  // bytes of a staging tile
+        const bool twice = 2 * outs * STG <= EPI_SMEM;
+        const bool res = FWD && !GLU && p.e.R != nullptr;
         int buf = 0, sb = 0;
         uint32_t acc_phase = 0;
         for (int tile = pair; tile < num_tiles; tile += npairs) {
@@ -437,38 +459,42 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             for (int c0 = 0; c0 < NT; c0 += 32) {
                 const int m0 = m_base + c0;
                 if (m0 >= p.M) break;
-                uint32_t v[32];
-                ptx::tmem_ld_32x32b_x32(tmem + lane_base + (uint32_t)(buf * 256 + c0), v);
-                ptx::tmem_wait_ld();
-                if (p.tma_out) {
-                    // the staging tiles written below were last read by the
-                    // stores of the chunk before last (or the last one)
-                    if (et == 0) {
-                        if (twice) tcp::bulk_wait_read_1();
-                        else bulk_wait_read_0();
-                    }
-                    ptx::bar_sync(1, 128);
+                // the staging tiles written below were last read by the stores
+                // of the chunk before last (or of the last one)
+                if (et == 0) {
+                    if (twice) tcp::bulk_wait_read_1();
+                    else bulk_wait_read_0();
                 }
-                T *stg = p.tma_out ? reinterpret_cast<T *>(sm.epi) + (twice ? sb * outs * STG : 0) : nullptr;
-                const Out<T> y = {stg, static_cast<T *>(p.e.Y), p.e.ldy};
-                if constexpr (FWD) {
-                    const Out<T> z = {stg ? stg + STG : nullptr, static_cast<T *>(p.e.Z), p.e.ldz};
-                    const Out<T> u = {stg ? stg + 2 * STG : nullptr, static_cast<T *>(p.e.U), p.e.ldz};
-                    const T *R = static_cast<const T *>(p.e.R);
-#define W4A8_CHUNK(A) \
-    fwd_chunk<A, GLU, T>(v, sm.tok + c0, rsw, b, lane, col, m0, p.M, n, n_ok, y, z, u, R, p.e.ldr)
-                    switch (p.act) {
-                        case W4A8_ACT_NONE: W4A8_CHUNK(W4A8_ACT_NONE); break;
-                        case W4A8_ACT_RELU: W4A8_CHUNK(W4A8_ACT_RELU); break;
-                        case W4A8_ACT_SILU: W4A8_CHUNK(W4A8_ACT_SILU); break;
-                        case W4A8_ACT_GELU: W4A8_CHUNK(W4A8_ACT_GELU); break;
-                        default: W4A8_CHUNK(W4A8_ACT_GELU_TANH); break;
-                    }
-#undef W4A8_CHUNK
-                } else {
+                ptx::bar_sync(1, 128);
+                uint8_t *stg = sm.epi + (twice ? sb * outs * STG : 0);
+#pragma unroll 1
+                for (int h = 0; h < 32; h += 16) {
+                    const uint32_t st = ptx::smem_addr(stg) + (uint32_t)((h * COLS + col) * (int)sizeof(T));
+                    uint32_t v[16];
+                    float r[16];
+                    if (res) {  // indexes past the edges repeat the last row or column
+                        const T *R = static_cast<const T *>(p.e.R) + min(n, p.N - 1);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        y.put(j, col, COLS, m0 + j, n, n_ok && m0 + j < p.M, __uint_as_float(v[j]) * sm.tok[c0 + j]);
+                        for (int j = 0; j < 16; ++j) r[j] = ld_elem(R + (size_t)min(m0 + h + j, p.M - 1) * p.e.ldr);
+                    }
+                    ptx::tmem_ld_32x32b_x16(tmem + lane_base + (uint32_t)(buf * 256 + c0 + h), v);
+                    ptx::tmem_wait_ld();
+                    const float *tok = sm.tok + c0 + h;
+                    if constexpr (FWD) {
+#define W4A8_HALF(A) fwd_half_any<A, GLU, T>(p.e.Z != nullptr, res, v, r, tok, rsw, b, lane, st, STG)
+                        switch (p.act) {
+                            case W4A8_ACT_NONE: W4A8_HALF(W4A8_ACT_NONE); break;
+                            case W4A8_ACT_RELU: W4A8_HALF(W4A8_ACT_RELU); break;
+                            case W4A8_ACT_SILU: W4A8_HALF(W4A8_ACT_SILU); break;
+                            case W4A8_ACT_GELU: W4A8_HALF(W4A8_ACT_GELU); break;
+                            default: W4A8_HALF(W4A8_ACT_GELU_TANH); break;
+                        }
+#undef W4A8_HALF
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sts_elem(st + j * COLS * (int)sizeof(T), __uint_as_float(v[j]) * tok[j], T());
+                    }
                 }
                 if (p.tma_out) {
                     tcp::fence_proxy_async_smem();  // the staging writes, before the store reads them
@@ -479,8 +505,13 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                         if (outs > 2) tcp::tma_store_2d(&tm_u, stg + 2 * STG, n_base, m0);
                         tcp::bulk_commit_group();
                     }
-                    sb ^= 1;
+                } else {
+                    ptx::bar_sync(1, 128);
+                    copy_out<COLS, T>(stg, p.e.Y, p.e.ldy, m0, p.M, n_base, p.N, et);
+                    if (outs > 1) copy_out<COLS, T>(stg + STG, p.e.Z, p.e.ldz, m0, p.M, n_base, p.N, et);
+                    if (outs > 2) copy_out<COLS, T>(stg + 2 * STG, p.e.U, p.e.ldz, m0, p.M, n_base, p.N, et);
                 }
+                sb ^= 1;
             }
             ptx::tc_fence_before();
             __syncwarp();
