@@ -49,7 +49,8 @@ enum { FWD_LINEAR = 0, FWD_GLU = 1, BWD_ONE = 2, BWD_TWO = 3 };  // BWD_TWO: two
 constexpr int ROWS_CTA = 128;              // A rows per CTA
 constexpr int A_BYTES = ROWS_CTA * 128;    // a widened slot: 128 rows x 128 k INT8, or 128 k x 64 n FP16
 constexpr int EPI_SMEM = 32768;            // output staging
-constexpr int CONV_WARPS = 8;
+constexpr int CONV_GROUPS = 2, GROUP_WARPS = 4;  // each group widens every second stage
+constexpr int CONV_WARPS = CONV_GROUPS * GROUP_WARPS;
 constexpr int FIRST_CONV = 4, FIRST_EPI = FIRST_CONV + CONV_WARPS;
 constexpr int PAIR_THREADS = 32 * (FIRST_EPI + 4);
 
@@ -77,7 +78,7 @@ struct alignas(1024) PairSmem {
     uint8_t epi[EPI_SMEM];
     uint64_t full[S::RAW];        // this CTA's TMA landed
     uint64_t empty[S::RAW];       // MMAs reading the stage finished (both CTAs)
-    uint64_t ready[S::A_SLOTS];   // leader: both CTAs' slots widened (16 warps)
+    uint64_t ready[S::A_SLOTS];   // leader: both CTAs' slots widened (8 warps)
     uint64_t acc_full[2];         // accumulator ready (both CTAs)
     uint64_t acc_empty[2];        // leader: both CTAs' epilogues drained (8 warps)
     uint64_t done;                // every MMA finished (both CTAs)
@@ -140,46 +141,53 @@ __device__ __forceinline__ void sts128(void *p, uint32_t a, uint32_t b, uint32_t
 }
 
 // ---------------------------------------------------------------- widening ---
-// Forward: A row r of this CTA (thread r, one of two halves of its 64 packed
-// bytes). The packed tile is a 64-byte swizzled box (16-byte chunk c of row s
-// at chunk c ^ ((s >> 1) & 3)); the slot is 128-byte swizzled. Nibbles stay in
-// the high half of their byte (16 q), in the order the INT8 rows are stored in.
+// Forward: A row r of this CTA, one per thread of a group. The packed tile is
+// a 64-byte swizzled box (16-byte chunk c of row s at chunk c ^ ((s >> 1) & 3));
+// the slot is 128-byte swizzled. Nibbles stay in the high half of their byte
+// (16 q), in the order the INT8 rows are stored in.
 template <bool GLU>
-__device__ __forceinline__ void widen_fwd(const uint8_t *packed, uint8_t *slot, int tid) {
-    const int r = tid & 127, half = tid >> 7;
+__device__ __forceinline__ void widen_fwd(const uint8_t *packed, uint8_t *slot, int r) {
     // gated: rows 32 w + 0..15 are gate channels 16 w + .., 32 w + 16..31 the same up channels
     const int s = GLU ? ((r & 16) << 2) + ((r >> 5) << 4) + (r & 15) : r;
+    uint4 v[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int c = 2 * half + i;
-        const uint4 v = ptx::lds128(packed + s * 64 + 16 * (c ^ ((s >> 1) & 3)));
-        uint8_t *row = slot + r * 128;
-        constexpr uint32_t H = 0xF0F0F0F0u;
-        sts128(row + 16 * ((2 * c) ^ (r & 7)), (v.x << 4) & H, v.x & H, (v.y << 4) & H, v.y & H);
-        sts128(row + 16 * ((2 * c + 1) ^ (r & 7)), (v.z << 4) & H, v.z & H, (v.w << 4) & H, v.w & H);
+    for (int c = 0; c < 4; ++c) v[c] = ptx::lds128(packed + s * 64 + 16 * (c ^ ((s >> 1) & 3)));
+    uint8_t *row = slot + r * 128;
+    constexpr uint32_t H = 0xF0F0F0F0u;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        sts128(row + 16 * ((2 * c) ^ (r & 7)), (v[c].x << 4) & H, v[c].x & H, (v[c].y << 4) & H, v[c].y & H);
+        sts128(row + 16 * ((2 * c + 1) ^ (r & 7)), (v[c].z << 4) & H, v[c].z & H, (v[c].w << 4) & H, v[c].w & H);
     }
 }
 
-// Gradient: packed row n (one n, 128 k), 16-byte chunk c = 32 codes. Nibble u
-// of q + 8 is put under the FP16 exponent of 1024 (1024 + u, exact) and 1032
-// is subtracted. Masking words of eight codes gives them in the order
-// k0 k4 k1 k5 k2 k6 k3 k7, undone by the epilogue's row index.
+// Gradient: packed row n (one n, 128 k), two 16-byte chunks of 32 codes per
+// thread. Nibble u of q + 8 is put under the FP16 exponent of 1024 (1024 + u,
+// exact) and 1032 is subtracted. Masking words of eight codes gives them in
+// the order k0 k4 k1 k5 k2 k6 k3 k7, undone by the epilogue's row index.
 __device__ __forceinline__ void widen_bwd(const uint8_t *packed, uint8_t *slot, int tid) {
-    const int n = tid & 63, c = tid >> 6;
-    const uint4 v = ptx::lds128(packed + n * 64 + 16 * (c ^ ((n >> 1) & 3)));
-    const uint32_t p[4] = {v.x, v.y, v.z, v.w};
-    uint8_t *row = slot + (c >> 1) * (64 * 128) + n * 128;
+    const int n = tid & 63;
     const __half2 off = __floats2half2_rn(1032.0f, 1032.0f);
+    uint4 v[2];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        uint32_t o[4];
+    for (int i = 0; i < 2; ++i)
+        v[i] = ptx::lds128(packed + n * 64 + 16 * ((2 * i + (tid >> 6)) ^ ((n >> 1) & 3)));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            uint32_t t = ((p[w] >> (4 * j)) & 0x000F000Fu) ^ 0x64086408u;
-            const __half2 h = __hsub2(*reinterpret_cast<__half2 *>(&t), off);
-            o[j] = *reinterpret_cast<const uint32_t *>(&h);
+    for (int i = 0; i < 2; ++i) {
+        const int c = 2 * i + (tid >> 6);
+        const uint32_t p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint8_t *row = slot + i * (64 * 128) + n * 128;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t t = ((p[w] >> (4 * j)) & 0x000F000Fu) ^ 0x64086408u;
+                const __half2 h = __hsub2(*reinterpret_cast<__half2 *>(&t), off);
+                o[j] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            sts128(row + 16 * ((4 * (c & 1) + w) ^ (n & 7)), o[0], o[1], o[2], o[3]);
         }
-        sts128(row + 16 * ((4 * (c & 1) + w) ^ (n & 7)), o[0], o[1], o[2], o[3]);
     }
 }
 
@@ -283,7 +291,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             ptx::mbar_init(&sm.full[s], 1);
             ptx::mbar_init(&sm.empty[s], 1);
         }
-        for (int a = 0; a < A_SLOTS; ++a) ptx::mbar_init(&sm.ready[a], 2 * CONV_WARPS);
+        for (int a = 0; a < A_SLOTS; ++a) ptx::mbar_init(&sm.ready[a], 2 * GROUP_WARPS);
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&sm.acc_full[b], 1);
             ptx::mbar_init(&sm.acc_empty[b], 8);
@@ -403,24 +411,24 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         }
     } else if (warp >= FIRST_CONV && warp < FIRST_EPI) {
         // ---------------------------------------------------- widening (each CTA: its 128 rows)
-        const int tid = threadIdx.x - 32 * FIRST_CONV;
-        int slot = 0, as = 0, old = 0;        // old: the stage slot of iteration it - A_SLOTS
-        uint32_t phase = 0, ophase = 0;
-        for (int it = 0; it < total; ++it) {
+        const int grp = (warp - FIRST_CONV) / GROUP_WARPS;
+        const int tid = (threadIdx.x - 32 * FIRST_CONV) % (32 * GROUP_WARPS);
+        int slot = grp, as = grp % A_SLOTS;
+        int old = (grp - A_SLOTS + RAW) % RAW;  // the stage slot of iteration it - A_SLOTS
+        uint32_t phase = 0, ophase = 1;         // old is below 0 at first: its phase flips as it wraps
+        for (int it = grp; it < total; it += CONV_GROUPS) {
             bool got = ptx::mbar_wait(&sm.full[slot], phase, abort);
             // the A slot was last read by the MMAs of iteration it - A_SLOTS
-            if (it >= A_SLOTS) {
-                got = got && ptx::mbar_wait(&sm.empty[old], ophase, abort);
-                if (++old == RAW) { old = 0; ophase ^= 1u; }
-            }
+            if (it >= A_SLOTS) got = got && ptx::mbar_wait(&sm.empty[old], ophase, abort);
             if (!__all_sync(0xffffffffu, got)) break;
             if constexpr (FWD) widen_fwd<GLU>(sm.packed[slot], sm.a[as], tid);
             else widen_bwd(sm.packed[slot], sm.a[as], tid);
             tcp::fence_proxy_async_smem();  // the slot's generic writes, before the MMA reads them
             __syncwarp();
             if (lane == 0) tcp::mbar_arrive_leader(&sm.ready[as]);
-            if (++slot == RAW) { slot = 0; phase ^= 1u; }
-            if (++as == A_SLOTS) as = 0;
+            if ((slot += CONV_GROUPS) >= RAW) { slot -= RAW; phase ^= 1u; }
+            if ((old += CONV_GROUPS) >= RAW) { old -= RAW; ophase ^= 1u; }
+            if ((as += CONV_GROUPS) >= A_SLOTS) as -= A_SLOTS;
         }
     } else if (warp >= FIRST_EPI) {
         // ---------------------------------------------------- epilogue (each CTA: its 128 TMEM lanes)
