@@ -80,7 +80,8 @@ w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a
     w4a8_status st = launch_quant_rows<T>(X, M, K, ldx, ws, flags, s);
     if (st != W4A8_OK) return st;
     if (path == W4A8_PATH_TC) {
-        const mlp::PairArgs p = {M, N, (K + 127) / 128, 0, ws.sx, a, b, ea, act, 0,
+        const int stages = (K + 255) / 256;
+        const mlp::PairArgs p = {M, N, K, stages, stages, ws.sx, a, b, ea, act, 0,
                                  (flags & W4A8_STATIC_WEIGHTS) != 0};
         const mlp::PairCall c = {a.Wp, b.Wp, N, ldp, ws.xq, M, ws.ldq, device_info().sm_count};
         st = mlp::launch_pair_any<GLU ? mlp::FWD_GLU : mlp::FWD_LINEAR, T>(p, c, s);
@@ -136,7 +137,7 @@ struct GradWorkspace {
 
 GradWorkspace grad_layout(int M, int N, int segs, unsigned flags) {
     GradWorkspace g = {};
-    g.seg = round_up(N, 64);
+    g.seg = round_up(N, 128);
     g.planes = io_bf16(flags) ? 1 : 2;
     g.p_bytes = round256((size_t)g.planes * M * segs * g.seg * sizeof(__half));
     g.rs_bytes = round256((size_t)M * sizeof(float));
@@ -173,8 +174,8 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
     });
     if (st != W4A8_OK) return st;
     if (path == W4A8_PATH_TC) {
-        const int seg_stages = ws.seg / 64;
-        const mlp::PairArgs p = {M, K, SEGS * seg_stages, seg_stages, ws.rs, {}, {},
+        const int seg_stages = ws.seg / (LO ? 64 : 128);
+        const mlp::PairArgs p = {M, K, N, seg_stages, SEGS * seg_stages, ws.rs, {}, {},
                                  {nullptr, dX, nullptr, nullptr, 0, lddx, 0}, 0, 0,
                                  (flags & W4A8_STATIC_WEIGHTS) != 0};
         const mlp::PairCall c = {Wa, Wb, N, ldp, ws.P, ws.planes * M, SEGS * ws.seg, device_info().sm_count};

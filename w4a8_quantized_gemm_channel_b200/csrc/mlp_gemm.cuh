@@ -24,12 +24,12 @@
 // shared memory: A and B reads of 4 KB each, 4 KB of B arriving, 2 KB (1 KB) of
 // packed weights in and out, 4 KB of widened weights written.
 //
-// Per CTA: 128 rows of A and half of the tile's tokens. Two rings: RAW stages
-// (packed weights and B, by TMA) and A slots (widened weights). Warp 0 loads,
-// warp 1 issues the MMAs (in the leader), warps 4-11 widen, warps 12-15 run
-// the epilogue of one tile while the next one's MMAs run (two accumulators).
-// No load is multicast. Every wait is bounded, as in gemm_tc_pair.cuh, whose
-// pair protocol this follows.
+// Per CTA: 128 rows of A and half of the tile's tokens. Three rings: packed
+// weights and tokens (TMA, freed by the widening and by the MMAs), widened
+// weights. Warp 0 loads weights, warp 2 tokens, warp 1 issues the MMAs (in the
+// leader), warps 4-11 widen, warps 12-15 run the epilogue of one tile while the
+// next one's MMAs run (two accumulators). No load is multicast. Every wait is
+// bounded, as in gemm_tc_pair.cuh, whose pair protocol this follows.
 //
 // Gated rows. The 32 TMEM lanes of an epilogue warp hold 16 gate and the same
 // 16 up channels (the widening warps place the rows so), and one shuffle per
@@ -46,39 +46,48 @@ namespace mlp {
 
 enum { FWD_LINEAR = 0, FWD_GLU = 1, BWD_ONE = 2, BWD_TWO = 3 };  // BWD_TWO: two planes of B (float32 rows)
 
-constexpr int ROWS_CTA = 128;              // A rows per CTA
-constexpr int A_BYTES = ROWS_CTA * 128;    // a widened slot: 128 rows x 128 k INT8, or 128 k x 64 n FP16
-constexpr int EPI_SMEM = 32768;            // output staging
-constexpr int CONV_GROUPS = 2, GROUP_WARPS = 4;  // each group widens every second stage
+constexpr int ROWS_CTA = 128;                  // A rows per CTA
+constexpr int SUB_BYTES = ROWS_CTA * 128;      // widened sub-tile: 128 rows x 128 k INT8, or 128 k x 64 n FP16
+constexpr int EPI_SMEM = 32768;                // output staging
+constexpr int CONV_GROUPS = 2, GROUP_WARPS = 4;
 constexpr int CONV_WARPS = CONV_GROUPS * GROUP_WARPS;
 constexpr int FIRST_CONV = 4, FIRST_EPI = FIRST_CONV + CONV_WARPS;
 constexpr int PAIR_THREADS = 32 * (FIRST_EPI + 4);
 
+// A stage is 8 MMAs: two sub-tiles of the contraction (128 k, or 64 n, each),
+// or one sub-tile against two planes. (With stages of 4 MMAs the issuing
+// thread's wait and commit per stage left the pipe idle a fifth of the time.)
 template <int MODE, int NT>
 struct Shape {
     static constexpr bool FWD = MODE == FWD_LINEAR || MODE == FWD_GLU;
     static constexpr int PLANES = MODE == BWD_TWO ? 2 : 1;
-    static constexpr int STEP = FWD ? 128 : 64;                 // contraction per stage
-    static constexpr int PACKED = FWD ? 128 * 64 : 64 * 64;     // packed bytes per stage
-    static constexpr int B_PLANE = NT / 2 * 128;
-    static constexpr int B_BYTES = PLANES * B_PLANE;
-    static constexpr int A_SLOTS = NT == 256 ? (MODE == BWD_TWO ? 2 : 3) : 4;
-    static constexpr int TABLES = 3072;                         // barriers and token tables
-    static constexpr int FIT = (232448 - 1024 - EPI_SMEM - TABLES - A_SLOTS * A_BYTES) / (PACKED + B_BYTES);
-    static constexpr int RAW = FIT < 8 ? FIT : 8;
-    static_assert(RAW >= A_SLOTS, "A-slot reuse waits on a stage barrier");
+    static constexpr int SUBS = 2 / PLANES;
+    static constexpr int SUB = FWD ? 128 : 64;                  // contraction per sub-tile
+    static constexpr int STEP = SUBS * SUB;                     // contraction per stage
+    static constexpr int P_SUB = FWD ? 128 * 64 : 64 * 64;      // packed bytes per sub-tile
+    static constexpr int P_BYTES = SUBS * P_SUB;
+    static constexpr int A_BYTES = SUBS * SUB_BYTES;
+    static constexpr int B_TILE = NT / 2 * 128;                 // one sub-tile or plane of the tokens
+    static constexpr int B_BYTES = 2 * B_TILE;
+    // Slots per ring. 256 tokens leave shared memory for two widened stages.
+    static constexpr int A_SLOTS = NT == 256 && SUBS == 2 ? 2 : 3;
+    static constexpr int P_SLOTS = NT == 256 ? 2 : 3;
+    static constexpr int B_SLOTS = NT == 64 ? 4 : 3;
+    static_assert(B_SLOTS >= A_SLOTS, "A-slot reuse waits on a token slot's barrier");
 };
 
 template <int MODE, int NT>
 struct alignas(1024) PairSmem {
     using S = Shape<MODE, NT>;
-    uint8_t b[S::RAW][S::B_BYTES];
-    uint8_t a[S::A_SLOTS][A_BYTES];
-    uint8_t packed[S::RAW][S::PACKED];
+    uint8_t b[S::B_SLOTS][S::B_BYTES];
+    uint8_t a[S::A_SLOTS][S::A_BYTES];
+    uint8_t packed[S::P_SLOTS][S::P_BYTES];
     uint8_t epi[EPI_SMEM];
-    uint64_t full[S::RAW];        // this CTA's TMA landed
-    uint64_t empty[S::RAW];       // MMAs reading the stage finished (both CTAs)
-    uint64_t ready[S::A_SLOTS];   // leader: both CTAs' slots widened (8 warps)
+    uint64_t pfull[S::P_SLOTS];   // packed weights landed
+    uint64_t pfree[S::P_SLOTS];   // packed weights read (8 widening warps)
+    uint64_t bfull[S::B_SLOTS];   // this CTA's tokens landed
+    uint64_t empty[S::B_SLOTS];   // MMAs of the stage finished (both CTAs)
+    uint64_t ready[S::A_SLOTS];   // leader: both CTAs' operands there (16 warps)
     uint64_t acc_full[2];         // accumulator ready (both CTAs)
     uint64_t acc_empty[2];        // leader: both CTAs' epilogues drained (8 warps)
     uint64_t done;                // every MMA finished (both CTAs)
@@ -90,8 +99,9 @@ struct alignas(1024) PairSmem {
 struct PairArgs {
     int M;              // tokens
     int N;              // rows of D: channels per projection, or K of the gradient
-    int stages;         // contraction stages per tile
-    int seg_stages;     // gradient: stages per segment
+    int depth;          // contraction per segment: K, or the gradient's N
+    int seg_stages;     // stages per segment
+    int stages;         // stages per tile (one segment, or two: the gated gradient)
     const float *tok;   // sx, or the rows' powers of two
     Proj a, b;
     EpiArgs e;          // gradient: Y = dX
@@ -161,34 +171,35 @@ __device__ __forceinline__ void widen_fwd(const uint8_t *packed, uint8_t *slot, 
     }
 }
 
-// Gradient: packed row n (one n, 128 k), two 16-byte chunks of 32 codes per
-// thread. Nibble u of q + 8 is put under the FP16 exponent of 1024 (1024 + u,
-// exact) and 1032 is subtracted. Masking words of eight codes gives them in
-// the order k0 k4 k1 k5 k2 k6 k3 k7, undone by the epilogue's row index.
-__device__ __forceinline__ void widen_bwd(const uint8_t *packed, uint8_t *slot, int tid) {
-    const int n = tid & 63;
+// Gradient: packed row n (one n, 128 k), 16-byte chunk c of 32 codes. Nibble u
+// of q + 8 is put under the FP16 exponent of 1024 (1024 + u, exact) and 1032
+// is subtracted. Masking words of eight codes gives them in the order
+// k0 k4 k1 k5 k2 k6 k3 k7, undone by the epilogue's row index.
+__device__ __forceinline__ void widen_chunk(const uint4 &v, uint8_t *slot, int n, int c) {
     const __half2 off = __floats2half2_rn(1032.0f, 1032.0f);
-    uint4 v[2];
+    const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+    uint8_t *row = slot + (c >> 1) * (64 * 128) + n * 128;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        v[i] = ptx::lds128(packed + n * 64 + 16 * ((2 * i + (tid >> 6)) ^ ((n >> 1) & 3)));
+    for (int w = 0; w < 4; ++w) {
+        uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int c = 2 * i + (tid >> 6);
-        const uint32_t p[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint8_t *row = slot + i * (64 * 128) + n * 128;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t t = ((p[w] >> (4 * j)) & 0x000F000Fu) ^ 0x64086408u;
-                const __half2 h = __hsub2(*reinterpret_cast<__half2 *>(&t), off);
-                o[j] = *reinterpret_cast<const uint32_t *>(&h);
-            }
-            sts128(row + 16 * ((4 * (c & 1) + w) ^ (n & 7)), o[0], o[1], o[2], o[3]);
+        for (int j = 0; j < 4; ++j) {
+            uint32_t t = ((p[w] >> (4 * j)) & 0x000F000Fu) ^ 0x64086408u;
+            const __half2 h = __hsub2(*reinterpret_cast<__half2 *>(&t), off);
+            o[j] = *reinterpret_cast<const uint32_t *>(&h);
         }
+        sts128(row + 16 * ((4 * (c & 1) + w) ^ (n & 7)), o[0], o[1], o[2], o[3]);
     }
+}
+__device__ __forceinline__ uint4 packed_chunk(const uint8_t *packed, int n, int c) {
+    return ptx::lds128(packed + n * 64 + 16 * (c ^ ((n >> 1) & 3)));
+}
+// A whole sub-tile by one group, or (two planes, one sub-tile) half of it.
+__device__ __forceinline__ void widen_bwd(const uint8_t *packed, uint8_t *slot, int tid) {
+    const int n = tid & 63, c = tid >> 6;
+    const uint4 v0 = packed_chunk(packed, n, c), v1 = packed_chunk(packed, n, c + 2);
+    widen_chunk(v0, slot, n, c);
+    widen_chunk(v1, slot, n, c + 2);
 }
 
 // ---------------------------------------------------------------- epilogue ---
@@ -273,7 +284,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
            const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_u, const PairArgs p) {
     using S = Shape<MODE, NT>;
     constexpr bool FWD = S::FWD, GLU = MODE == FWD_GLU;
-    constexpr int RAW = S::RAW, A_SLOTS = S::A_SLOTS, HT = NT / 2;
+    constexpr int A_SLOTS = S::A_SLOTS, B_SLOTS = S::B_SLOTS, HT = NT / 2;
     constexpr int TILE_ROWS = GLU ? ROWS_CTA : 2 * ROWS_CTA;  // output columns per pair tile
     extern __shared__ uint8_t smem_raw[];
     auto &sm = *reinterpret_cast<PairSmem<MODE, NT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -287,11 +298,15 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
     volatile int *abort = &sm.abort;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < RAW; ++s) {
-            ptx::mbar_init(&sm.full[s], 1);
+        for (int s = 0; s < S::P_SLOTS; ++s) {
+            ptx::mbar_init(&sm.pfull[s], 1);
+            ptx::mbar_init(&sm.pfree[s], CONV_WARPS);
+        }
+        for (int s = 0; s < B_SLOTS; ++s) {
+            ptx::mbar_init(&sm.bfull[s], 1);
             ptx::mbar_init(&sm.empty[s], 1);
         }
-        for (int a = 0; a < A_SLOTS; ++a) ptx::mbar_init(&sm.ready[a], 2 * GROUP_WARPS);
+        for (int a = 0; a < A_SLOTS; ++a) ptx::mbar_init(&sm.ready[a], 2 * CONV_WARPS);
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&sm.acc_full[b], 1);
             ptx::mbar_init(&sm.acc_empty[b], 8);
@@ -313,25 +328,29 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
-    // Packed weights of stage st of a tile (its full barrier then also waits
-    // for the tokens' tile).
+    // Packed weights of stage st of a tile. Sub-tiles past the contraction's
+    // end are zero-filled by the loads' bounds.
     auto load_weights = [&](int slot, int n_tile, int st) {
-        ptx::mbar_arrive_expect_tx(&sm.full[slot], S::PACKED + S::B_BYTES);
-        if constexpr (MODE == FWD_LINEAR) {
-            ptx::tma_load_2d(sm.packed[slot], &tm_wa, 64 * st, n_tile * 256 + rank * 128, &sm.full[slot]);
-        } else if constexpr (GLU) {
-            const int n0 = n_tile * 128 + rank * 64;
-            ptx::tma_load_2d(sm.packed[slot], &tm_wa, 64 * st, n0, &sm.full[slot]);
-            ptx::tma_load_2d(sm.packed[slot] + 4096, &tm_wb, 64 * st, n0, &sm.full[slot]);
-        } else {
-            const bool second = st >= p.seg_stages;
-            ptx::tma_load_2d(sm.packed[slot], second ? &tm_wb : &tm_wa, n_tile * 128 + rank * 64,
-                             64 * (second ? st - p.seg_stages : st), &sm.full[slot]);
+        ptx::mbar_arrive_expect_tx(&sm.pfull[slot], S::P_BYTES);
+#pragma unroll
+        for (int u = 0; u < S::SUBS; ++u) {
+            uint8_t *dst = sm.packed[slot] + u * S::P_SUB;
+            if constexpr (MODE == FWD_LINEAR) {
+                ptx::tma_load_2d(dst, &tm_wa, 64 * (S::SUBS * st + u), n_tile * 256 + rank * 128, &sm.pfull[slot]);
+            } else if constexpr (GLU) {
+                const int n0 = n_tile * 128 + rank * 64;
+                ptx::tma_load_2d(dst, &tm_wa, 64 * (S::SUBS * st + u), n0, &sm.pfull[slot]);
+                ptx::tma_load_2d(dst + 4096, &tm_wb, 64 * (S::SUBS * st + u), n0, &sm.pfull[slot]);
+            } else {
+                const bool second = st >= p.seg_stages;
+                ptx::tma_load_2d(dst, second ? &tm_wb : &tm_wa, n_tile * 128 + rank * 64,
+                                 64 * (S::SUBS * (second ? st - p.seg_stages : st) + u), &sm.pfull[slot]);
+            }
         }
     };
     // Static weights: the first stages' packed tiles are requested before the
     // dependency wait; the tokens are read only after it.
-    const int pre_w = p.static_w ? min(RAW, total) : 0;
+    const int pre_w = p.static_w ? min(S::P_SLOTS, total) : 0;
     if (warp == 0 && lane == 0)
         for (int it = 0; it < pre_w; ++it)
             load_weights(it, (pair + (it / p.stages) * npairs) / tiles_m, it % p.stages);
@@ -339,70 +358,95 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
     griddep_launch_dependents();
     griddep_wait();
 
-    if (warp == 0) {
-        // ---------------------------------------------------- TMA producer (each CTA: its halves)
+    if (warp == 0 || warp == 2) {
+        // ------------------------------------- TMA producers (each CTA: its halves)
+        // Warp 0: packed weights, freed as soon as they are widened. Warp 2:
+        // tokens, freed by the MMAs.
         if (lane == 0) {
+            const bool w = warp == 0;
+            const int slots = w ? S::P_SLOTS : B_SLOTS;
+            uint64_t *full = w ? sm.pfull : sm.bfull, *freed = w ? sm.pfree : sm.empty;
             int slot = 0, it = 0;
-            uint32_t phase = 0, issued = 0, last_par = 0;
+            uint32_t phase = 0, issued = (1u << pre_w) - 1u, last_par = 0;
+            if (!w) issued = 0;
             bool ok = true;
             for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-                const int n_tile = tile / tiles_m, m_tile = tile % tiles_m;
-                const int m0 = m_tile * NT + rank * HT;
+                const int n_tile = tile / tiles_m;
+                const int m0 = (tile % tiles_m) * NT + rank * HT;
                 for (int st = 0; st < p.stages; ++st, ++it) {
-                    if (it >= pre_w) {
-                        if (!ptx::mbar_wait(&sm.empty[slot], phase ^ 1, abort)) { ok = false; break; }
-                        load_weights(slot, n_tile, st);
-                    }
+                    if (!w || it >= pre_w) {
+                        if (!ptx::mbar_wait(&freed[slot], phase ^ 1, abort)) { ok = false; break; }
+                        if (w) {
+                            load_weights(slot, n_tile, st);
+                        } else {
+                            ptx::mbar_arrive_expect_tx(&sm.bfull[slot], S::B_BYTES);
 #pragma unroll
-                    for (int pl = 0; pl < S::PLANES; ++pl)
-                        ptx::tma_load_2d(sm.b[slot] + pl * S::B_PLANE, &tm_x, S::STEP * st, pl * p.M + m0,
-                                         &sm.full[slot]);
+                            for (int u = 0; u < 2; ++u)
+                                ptx::tma_load_2d(sm.b[slot] + u * S::B_TILE, &tm_x,
+                                                 S::STEP * st + (S::SUBS == 2 ? u * S::SUB : 0),
+                                                 m0 + (S::PLANES == 2 ? u * p.M : 0), &sm.bfull[slot]);
+                        }
+                    }
                     issued |= 1u << slot;
                     last_par = (last_par & ~(1u << slot)) | (phase << slot);
-                    if (++slot == RAW) { slot = 0; phase ^= 1; }
+                    if (++slot == slots) { slot = 0; phase ^= 1; }
                 }
             }
             // Drain: every load this thread issued lands before the CTA exits.
             if (!ok)
-                for (int s = 0; s < RAW; ++s)
-                    if (issued & (1u << s)) ptx::mbar_wait_drain(&sm.full[s], (last_par >> s) & 1u);
+                for (int s = 0; s < slots; ++s)
+                    if (issued & (1u << s)) ptx::mbar_wait_drain(&full[s], (last_par >> s) & 1u);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------- MMA issuer (leader only)
-        // The widening warps of both CTAs arrive on ready only after their own
-        // wait on full[] of the same stage, so both CTAs' token halves have
-        // landed too once it flips.
+        // The widening warps of both CTAs arrive on ready only after the
+        // tokens of the same stage have landed in their CTA.
         if (rank == 0 && lane == 0) {
             constexpr uint32_t idesc = FWD ? ptx::idesc_i8(256, NT) : idesc_f16_mn(256, NT);
-            int slot = 0, as = 0, st = 0, buf = 0;
+            // descriptors count 16-byte units, so a step is an addition
+            const uint64_t a0 = FWD ? ptx::sdesc_k_sw128(ptx::smem_addr(sm.a[0]))
+                                    : sdesc_mn_sw128(ptx::smem_addr(sm.a[0]), 64 * 128);
+            const uint64_t b0 = ptx::sdesc_k_sw128(ptx::smem_addr(sm.b[0]));
+            constexpr uint32_t A_STEP = FWD ? 32 : 2048;  // bytes per MMA along the contraction
+            int slot = 0, as = 0, st = 0, buf = 0, left = p.depth;
+            int seg_st = 0;
             uint32_t aphase = 0, bphase = 0;
             bool ok = total > 0 ? ptx::mbar_wait(&sm.ready[0], 0, abort) : true;
             for (int it = 0; it < total && ok; ++it) {
                 if (st == 0 && !ptx::mbar_wait(&sm.acc_empty[buf], bphase ^ 1u, abort)) break;
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * 256);
-                const uint32_t a = ptx::smem_addr(sm.a[as]), b = ptx::smem_addr(sm.b[slot]);
+                const uint64_t a = a0 + (uint32_t)(as * S::A_BYTES / 16), b = b0 + (uint32_t)(slot * S::B_BYTES / 16);
                 int nas = as + 1;
                 uint32_t naphase = aphase;
                 if (nas == A_SLOTS) { nas = 0; naphase ^= 1u; }
+                auto mma = [&](int i) {
+                    const int sub = S::SUBS == 2 ? i >> 2 : 0, kk = i & 3;
+                    mma_ss2<FWD>(d, a + (uint32_t)((sub * SUB_BYTES + kk * A_STEP) / 16),
+                                 b + (uint32_t)(((i >> 2) * S::B_TILE + 32 * kk) / 16), idesc, (st | i) != 0);
+                };
                 bool next_ok = true;
+                if (S::SUBS == 1 || left > S::SUB) {
 #pragma unroll
-                for (int pl = 0; pl < S::PLANES; ++pl)
+                    for (int i = 0; i < 7; ++i) mma(i);
+                    // wait for the next operands while the queued MMAs run
+                    if (it + 1 < total) next_ok = ptx::mbar_wait(&sm.ready[nas], naphase, abort);
+                    mma(7);
+                } else {  // the second sub-tile lies past the end of the contraction
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        // wait for the next operands while the queued MMAs run
-                        if (pl == S::PLANES - 1 && kk == 3 && it + 1 < total)
-                            next_ok = ptx::mbar_wait(&sm.ready[nas], naphase, abort);
-                        const uint64_t ad = FWD ? ptx::sdesc_k_sw128(a + 32 * kk) : sdesc_mn_sw128(a + 2048 * kk, 64 * 128);
-                        mma_ss2<FWD>(d, ad, ptx::sdesc_k_sw128(b + pl * S::B_PLANE + 32 * kk), idesc, (st | pl | kk) != 0);
-                    }
+                    for (int i = 0; i < 3; ++i) mma(i);
+                    if (it + 1 < total) next_ok = ptx::mbar_wait(&sm.ready[nas], naphase, abort);
+                    mma(3);
+                }
                 tcp::mma_commit2_both(&sm.empty[slot]);
+                left -= S::STEP;
+                if (++seg_st == p.seg_stages) { seg_st = 0; left = p.depth; }
                 if (++st == p.stages) {
                     tcp::mma_commit2_both(&sm.acc_full[buf]);
                     st = 0;
                     if (++buf == 2) { buf = 0; bphase ^= 1u; }
                 }
-                if (++slot == RAW) slot = 0;
+                if (++slot == B_SLOTS) slot = 0;
                 as = nas;
                 aphase = naphase;
                 ok = next_ok;
@@ -413,22 +457,30 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         // ---------------------------------------------------- widening (each CTA: its 128 rows)
         const int grp = (warp - FIRST_CONV) / GROUP_WARPS;
         const int tid = (threadIdx.x - 32 * FIRST_CONV) % (32 * GROUP_WARPS);
-        int slot = grp, as = grp % A_SLOTS;
-        int old = (grp - A_SLOTS + RAW) % RAW;  // the stage slot of iteration it - A_SLOTS
-        uint32_t phase = 0, ophase = 1;         // old is below 0 at first: its phase flips as it wraps
-        for (int it = grp; it < total; it += CONV_GROUPS) {
-            bool got = ptx::mbar_wait(&sm.full[slot], phase, abort);
+        int ps = 0, bs = 0, as = 0;
+        int old = B_SLOTS - A_SLOTS;    // the token slot of iteration it - A_SLOTS
+        uint32_t pphase = 0, bphase = 0, ophase = 1;  // it starts below 0: its phase flips as it wraps
+        for (int it = 0; it < total; ++it) {
+            bool got = ptx::mbar_wait(&sm.pfull[ps], pphase, abort);
             // the A slot was last read by the MMAs of iteration it - A_SLOTS
             if (it >= A_SLOTS) got = got && ptx::mbar_wait(&sm.empty[old], ophase, abort);
             if (!__all_sync(0xffffffffu, got)) break;
-            if constexpr (FWD) widen_fwd<GLU>(sm.packed[slot], sm.a[as], tid);
-            else widen_bwd(sm.packed[slot], sm.a[as], tid);
+            if constexpr (FWD)
+                widen_fwd<GLU>(sm.packed[ps] + grp * S::P_SUB, sm.a[as] + grp * SUB_BYTES, tid);
+            else if constexpr (S::SUBS == 2)
+                widen_bwd(sm.packed[ps] + grp * S::P_SUB, sm.a[as] + grp * SUB_BYTES, tid);
+            else
+                widen_chunk(packed_chunk(sm.packed[ps], tid & 63, 2 * grp + (tid >> 6)), sm.a[as], tid & 63,
+                            2 * grp + (tid >> 6));
             tcp::fence_proxy_async_smem();  // the slot's generic writes, before the MMA reads them
             __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sm.pfree[ps]);
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.bfull[bs], bphase, abort))) break;
             if (lane == 0) tcp::mbar_arrive_leader(&sm.ready[as]);
-            if ((slot += CONV_GROUPS) >= RAW) { slot -= RAW; phase ^= 1u; }
-            if ((old += CONV_GROUPS) >= RAW) { old -= RAW; ophase ^= 1u; }
-            if ((as += CONV_GROUPS) >= A_SLOTS) as -= A_SLOTS;
+            if (++ps == S::P_SLOTS) { ps = 0; pphase ^= 1u; }
+            if (++bs == B_SLOTS) { bs = 0; bphase ^= 1u; }
+            if (++old == B_SLOTS) { old = 0; ophase ^= 1u; }
+            if (++as == A_SLOTS) as = 0;
         }
     } else if (warp >= FIRST_EPI) {
         // ---------------------------------------------------- epilogue (each CTA: its 128 TMEM lanes)
