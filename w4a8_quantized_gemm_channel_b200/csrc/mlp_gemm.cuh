@@ -144,6 +144,17 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t bloc
     return d;
 }
 
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(v));
+    return v != 0;
+}
+// A bounded wait of the whole warp with one outcome for all its lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort));
+}
 __device__ __forceinline__ void bulk_wait_read_0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void sts128(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(ptx::smem_addr(p)), "r"(a), "r"(b), "r"(c), "r"(d)
@@ -288,7 +299,9 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
     constexpr int TILE_ROWS = GLU ? ROWS_CTA : 2 * ROWS_CTA;  // output columns per pair tile
     extern __shared__ uint8_t smem_raw[];
     auto &sm = *reinterpret_cast<PairSmem<MODE, NT> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // warp-uniform by construction, so that what the MMA warp computes from it
+    // stays on the uniform datapath, where tcgen05 takes its operands from
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = (int)ptx::cluster_ctarank();
     const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
     const int tiles_m = (p.M + NT - 1) / NT, tiles_n = (p.N + TILE_ROWS - 1) / TILE_ROWS;
@@ -326,7 +339,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
     ptx::cluster_arrive_release();
     ptx::cluster_wait_acquire();
     ptx::tc_fence_after();
-    const uint32_t tmem = sm.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
 
     // Packed weights of stage st of a tile. Sub-tiles past the contraction's
     // end are zero-filled by the loads' bounds.
@@ -401,7 +414,11 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         // ---------------------------------------------------- MMA issuer (leader only)
         // The widening warps of both CTAs arrive on ready only after the
         // tokens of the same stage have landed in their CTA.
-        if (rank == 0 && lane == 0) {
+        // The whole warp runs the loop and one elected lane issues: descriptors
+        // and addresses are then uniform values. (With one lane in a branch of
+        // its own each MMA took about 100 cycles to issue and a commit 400.)
+        if (rank == 0) {
+            const bool one = elect_one();
             constexpr uint32_t idesc = FWD ? ptx::idesc_i8(256, NT) : idesc_f16_mn(256, NT);
             // descriptors count 16-byte units, so a step is an addition
             const uint64_t a0 = FWD ? ptx::sdesc_k_sw128(ptx::smem_addr(sm.a[0]))
@@ -411,9 +428,9 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             int slot = 0, as = 0, st = 0, buf = 0, left = p.depth;
             int seg_st = 0;
             uint32_t aphase = 0, bphase = 0;
-            bool ok = total > 0 ? ptx::mbar_wait(&sm.ready[0], 0, abort) : true;
+            bool ok = total > 0 ? warp_wait(&sm.ready[0], 0, abort) : true;
             for (int it = 0; it < total && ok; ++it) {
-                if (st == 0 && !ptx::mbar_wait(&sm.acc_empty[buf], bphase ^ 1u, abort)) break;
+                if (st == 0 && !warp_wait(&sm.acc_empty[buf], bphase ^ 1u, abort)) break;
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * 256);
                 const uint64_t a = a0 + (uint32_t)(as * S::A_BYTES / 16), b = b0 + (uint32_t)(slot * S::B_BYTES / 16);
@@ -422,27 +439,28 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                 if (nas == A_SLOTS) { nas = 0; naphase ^= 1u; }
                 auto mma = [&](int i) {
                     const int sub = S::SUBS == 2 ? i >> 2 : 0, kk = i & 3;
-                    mma_ss2<FWD>(d, a + (uint32_t)((sub * SUB_BYTES + kk * A_STEP) / 16),
-                                 b + (uint32_t)(((i >> 2) * S::B_TILE + 32 * kk) / 16), idesc, (st | i) != 0);
+                    const uint64_t ad = a + (uint32_t)((sub * SUB_BYTES + kk * A_STEP) / 16);
+                    const uint64_t bd = b + (uint32_t)(((i >> 2) * S::B_TILE + 32 * kk) / 16);
+                    if (one) mma_ss2<FWD>(d, ad, bd, idesc, (st | i) != 0);
                 };
                 bool next_ok = true;
                 if (S::SUBS == 1 || left > S::SUB) {
 #pragma unroll
                     for (int i = 0; i < 7; ++i) mma(i);
                     // wait for the next operands while the queued MMAs run
-                    if (it + 1 < total) next_ok = ptx::mbar_wait(&sm.ready[nas], naphase, abort);
+                    if (it + 1 < total) next_ok = warp_wait(&sm.ready[nas], naphase, abort);
                     mma(7);
                 } else {  // the second sub-tile lies past the end of the contraction
 #pragma unroll
                     for (int i = 0; i < 3; ++i) mma(i);
-                    if (it + 1 < total) next_ok = ptx::mbar_wait(&sm.ready[nas], naphase, abort);
+                    if (it + 1 < total) next_ok = warp_wait(&sm.ready[nas], naphase, abort);
                     mma(3);
                 }
-                tcp::mma_commit2_both(&sm.empty[slot]);
+                if (one) tcp::mma_commit2_both(&sm.empty[slot]);
                 left -= S::STEP;
                 if (++seg_st == p.seg_stages) { seg_st = 0; left = p.depth; }
                 if (++st == p.stages) {
-                    tcp::mma_commit2_both(&sm.acc_full[buf]);
+                    if (one) tcp::mma_commit2_both(&sm.acc_full[buf]);
                     st = 0;
                     if (++buf == 2) { buf = 0; bphase ^= 1u; }
                 }
@@ -451,7 +469,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                 aphase = naphase;
                 ok = next_ok;
             }
-            if (total > 0) tcp::mma_commit2_both(&sm.done);
+            if (total > 0 && one) tcp::mma_commit2_both(&sm.done);
         }
     } else if (warp >= FIRST_CONV && warp < FIRST_EPI) {
         // ---------------------------------------------------- widening (each CTA: its 128 rows)
