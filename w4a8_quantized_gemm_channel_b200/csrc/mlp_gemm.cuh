@@ -162,30 +162,43 @@ __device__ __forceinline__ void sts128(void *p, uint32_t a, uint32_t b, uint32_t
 }
 
 // ---------------------------------------------------------------- widening ---
-// Forward: A row r of this CTA, one per thread of a group. The packed tile is
-// a 64-byte swizzled box (16-byte chunk c of row s at chunk c ^ ((s >> 1) & 3));
-// the slot is 128-byte swizzled. Nibbles stay in the high half of their byte
-// (16 q), in the order the INT8 rows are stored in.
-template <bool GLU>
-__device__ __forceinline__ void widen_fwd(const uint8_t *packed, uint8_t *slot, int r) {
-    // gated: rows 32 w + 0..15 are gate channels 16 w + .., 32 w + 16..31 the same up channels
-    const int s = GLU ? ((r & 16) << 2) + ((r >> 5) << 4) + (r & 15) : r;
-    uint4 v[4];
+// A thread's 16-byte pieces (32 codes) of a stage, in two steps: the loads and
+// the widening with its stores. A packed sub-tile is a 64-byte swizzled box
+// (16-byte chunk c of row s at chunk c ^ ((s >> 1) & 3)); widened sub-tiles
+// are 128-byte swizzled.
+//
+// Forward: group g takes sub-tile g, a thread one A row r. Nibbles stay in the
+// high half of their byte (16 q), in the order the INT8 rows are stored in.
+// Gated: A rows 32 w + 0..15 are gate channels 16 w + .., 32 w + 16..31 the
+// same up channels (the packed tile holds 64 gate rows, then 64 up rows).
+//
+// Gradient: a thread takes chunks c of packed row n (one n, 128 k): c = tid / 64
+// and that + 2 of sub-tile g, or with two planes (one sub-tile) c = 2 g + tid / 64.
+// Nibble u of q + 8 is put under the FP16 exponent of 1024 (1024 + u, exact)
+// and 1032 is subtracted. Masking words of eight codes gives them in the order
+// k0 k4 k1 k5 k2 k6 k3 k7, undone by the epilogue's row index.
+template <int MODE>
+constexpr int pieces() { return MODE == BWD_TWO ? 1 : MODE == BWD_ONE ? 2 : 4; }
+
+template <int MODE>
+__device__ __forceinline__ void load_pieces(uint4 (&v)[pieces<MODE>()], const uint8_t *packed, int g, int tid) {
+    if constexpr (MODE == FWD_LINEAR || MODE == FWD_GLU) {
+        const int r = tid, s = MODE == FWD_GLU ? ((r & 16) << 2) + ((r >> 5) << 4) + (r & 15) : r;
+        const uint8_t *row = packed + g * (128 * 64) + s * 64;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = ptx::lds128(packed + s * 64 + 16 * (c ^ ((s >> 1) & 3)));
-    uint8_t *row = slot + r * 128;
-    constexpr uint32_t H = 0xF0F0F0F0u;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        sts128(row + 16 * ((2 * c) ^ (r & 7)), (v[c].x << 4) & H, v[c].x & H, (v[c].y << 4) & H, v[c].y & H);
-        sts128(row + 16 * ((2 * c + 1) ^ (r & 7)), (v[c].z << 4) & H, v[c].z & H, (v[c].w << 4) & H, v[c].w & H);
+        for (int c = 0; c < 4; ++c) v[c] = ptx::lds128(row + 16 * (c ^ ((s >> 1) & 3)));
+    } else {
+        const int n = tid & 63, c = tid >> 6;
+        const uint8_t *row = packed + (MODE == BWD_ONE ? g * (64 * 64) : 0) + n * 64;
+        if constexpr (MODE == BWD_ONE) {
+            v[0] = ptx::lds128(row + 16 * (c ^ ((n >> 1) & 3)));
+            v[1] = ptx::lds128(row + 16 * ((c + 2) ^ ((n >> 1) & 3)));
+        } else {
+            v[0] = ptx::lds128(row + 16 * ((2 * g + c) ^ ((n >> 1) & 3)));
+        }
     }
 }
 
-// Gradient: packed row n (one n, 128 k), 16-byte chunk c of 32 codes. Nibble u
-// of q + 8 is put under the FP16 exponent of 1024 (1024 + u, exact) and 1032
-// is subtracted. Masking words of eight codes gives them in the order
-// k0 k4 k1 k5 k2 k6 k3 k7, undone by the epilogue's row index.
 __device__ __forceinline__ void widen_chunk(const uint4 &v, uint8_t *slot, int n, int c) {
     const __half2 off = __floats2half2_rn(1032.0f, 1032.0f);
     const uint32_t p[4] = {v.x, v.y, v.z, v.w};
@@ -202,15 +215,24 @@ __device__ __forceinline__ void widen_chunk(const uint4 &v, uint8_t *slot, int n
         sts128(row + 16 * ((4 * (c & 1) + w) ^ (n & 7)), o[0], o[1], o[2], o[3]);
     }
 }
-__device__ __forceinline__ uint4 packed_chunk(const uint8_t *packed, int n, int c) {
-    return ptx::lds128(packed + n * 64 + 16 * (c ^ ((n >> 1) & 3)));
-}
-// A whole sub-tile by one group, or (two planes, one sub-tile) half of it.
-__device__ __forceinline__ void widen_bwd(const uint8_t *packed, uint8_t *slot, int tid) {
-    const int n = tid & 63, c = tid >> 6;
-    const uint4 v0 = packed_chunk(packed, n, c), v1 = packed_chunk(packed, n, c + 2);
-    widen_chunk(v0, slot, n, c);
-    widen_chunk(v1, slot, n, c + 2);
+
+template <int MODE>
+__device__ __forceinline__ void widen_pieces(const uint4 (&v)[pieces<MODE>()], uint8_t *slot, int g, int tid) {
+    if constexpr (MODE == FWD_LINEAR || MODE == FWD_GLU) {
+        const int r = tid;
+        uint8_t *row = slot + g * SUB_BYTES + r * 128;
+        constexpr uint32_t H = 0xF0F0F0F0u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            sts128(row + 16 * ((2 * c) ^ (r & 7)), (v[c].x << 4) & H, v[c].x & H, (v[c].y << 4) & H, v[c].y & H);
+            sts128(row + 16 * ((2 * c + 1) ^ (r & 7)), (v[c].z << 4) & H, v[c].z & H, (v[c].w << 4) & H, v[c].w & H);
+        }
+    } else if constexpr (MODE == BWD_ONE) {
+        widen_chunk(v[0], slot + g * SUB_BYTES, tid & 63, tid >> 6);
+        widen_chunk(v[1], slot + g * SUB_BYTES, tid & 63, (tid >> 6) + 2);
+    } else {
+        widen_chunk(v[0], slot, tid & 63, 2 * g + (tid >> 6));
+    }
 }
 
 // ---------------------------------------------------------------- epilogue ---
@@ -428,33 +450,23 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             int slot = 0, as = 0, st = 0, buf = 0, left = p.depth;
             int seg_st = 0;
             uint32_t aphase = 0, bphase = 0;
-            bool ok = total > 0 ? warp_wait(&sm.ready[0], 0, abort) : true;
-            for (int it = 0; it < total && ok; ++it) {
+            for (int it = 0; it < total; ++it) {
                 if (st == 0 && !warp_wait(&sm.acc_empty[buf], bphase ^ 1u, abort)) break;
+                if (!warp_wait(&sm.ready[as], aphase, abort)) break;
                 ptx::tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(buf * 256);
                 const uint64_t a = a0 + (uint32_t)(as * S::A_BYTES / 16), b = b0 + (uint32_t)(slot * S::B_BYTES / 16);
-                int nas = as + 1;
-                uint32_t naphase = aphase;
-                if (nas == A_SLOTS) { nas = 0; naphase ^= 1u; }
                 auto mma = [&](int i) {
                     const int sub = S::SUBS == 2 ? i >> 2 : 0, kk = i & 3;
                     const uint64_t ad = a + (uint32_t)((sub * SUB_BYTES + kk * A_STEP) / 16);
                     const uint64_t bd = b + (uint32_t)(((i >> 2) * S::B_TILE + 32 * kk) / 16);
                     if (one) mma_ss2<FWD>(d, ad, bd, idesc, (st | i) != 0);
                 };
-                bool next_ok = true;
-                if (S::SUBS == 1 || left > S::SUB) {
 #pragma unroll
-                    for (int i = 0; i < 7; ++i) mma(i);
-                    // wait for the next operands while the queued MMAs run
-                    if (it + 1 < total) next_ok = warp_wait(&sm.ready[nas], naphase, abort);
-                    mma(7);
-                } else {  // the second sub-tile lies past the end of the contraction
+                for (int i = 0; i < 4; ++i) mma(i);
+                if (S::SUBS == 1 || left > S::SUB) {  // else the second sub-tile lies past the contraction's end
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) mma(i);
-                    if (it + 1 < total) next_ok = warp_wait(&sm.ready[nas], naphase, abort);
-                    mma(3);
+                    for (int i = 4; i < 8; ++i) mma(i);
                 }
                 if (one) tcp::mma_commit2_both(&sm.empty[slot]);
                 left -= S::STEP;
@@ -465,9 +477,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                     if (++buf == 2) { buf = 0; bphase ^= 1u; }
                 }
                 if (++slot == B_SLOTS) slot = 0;
-                as = nas;
-                aphase = naphase;
-                ok = next_ok;
+                if (++as == A_SLOTS) { as = 0; aphase ^= 1u; }
             }
             if (total > 0 && one) tcp::mma_commit2_both(&sm.done);
         }
@@ -479,21 +489,20 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         int old = B_SLOTS - A_SLOTS;    // the token slot of iteration it - A_SLOTS
         uint32_t pphase = 0, bphase = 0, ophase = 1;  // it starts below 0: its phase flips as it wraps
         for (int it = 0; it < total; ++it) {
-            bool got = ptx::mbar_wait(&sm.pfull[ps], pphase, abort);
-            // the A slot was last read by the MMAs of iteration it - A_SLOTS
-            if (it >= A_SLOTS) got = got && ptx::mbar_wait(&sm.empty[old], ophase, abort);
-            if (!__all_sync(0xffffffffu, got)) break;
-            if constexpr (FWD)
-                widen_fwd<GLU>(sm.packed[ps] + grp * S::P_SUB, sm.a[as] + grp * SUB_BYTES, tid);
-            else if constexpr (S::SUBS == 2)
-                widen_bwd(sm.packed[ps] + grp * S::P_SUB, sm.a[as] + grp * SUB_BYTES, tid);
-            else
-                widen_chunk(packed_chunk(sm.packed[ps], tid & 63, 2 * grp + (tid >> 6)), sm.a[as], tid & 63,
-                            2 * grp + (tid >> 6));
-            tcp::fence_proxy_async_smem();  // the slot's generic writes, before the MMA reads them
+            // The packed bytes come into registers, and their slot is free
+            // again, before the wait for the A slot: what follows the MMAs'
+            // end is only the widening and its stores.
+            if (!warp_wait(&sm.pfull[ps], pphase, abort)) break;
+            uint4 v[pieces<MODE>()];
+            load_pieces<MODE>(v, sm.packed[ps], grp, tid);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&sm.pfree[ps]);
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.bfull[bs], bphase, abort))) break;
+            if (!warp_wait(&sm.bfull[bs], bphase, abort)) break;
+            // the A slot was last read by the MMAs of iteration it - A_SLOTS
+            if (it >= A_SLOTS && !warp_wait(&sm.empty[old], ophase, abort)) break;
+            widen_pieces<MODE>(v, sm.a[as], grp, tid);
+            tcp::fence_proxy_async_smem();  // the slot's generic writes, before the MMA reads them
+            __syncwarp();
             if (lane == 0) tcp::mbar_arrive_leader(&sm.ready[as]);
             if (++ps == S::P_SLOTS) { ps = 0; pphase ^= 1u; }
             if (++bs == B_SLOTS) { bs = 0; bphase ^= 1u; }
