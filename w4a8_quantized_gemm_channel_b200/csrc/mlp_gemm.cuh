@@ -28,7 +28,7 @@
 // weights and tokens (TMA, freed by the widening and by the MMAs), widened
 // weights. Warp 0 loads weights, warp 2 tokens, warp 1 issues the MMAs (in the
 // leader), warps 4-11 widen, warps 12-15 run the epilogue of one tile while the
-// next one's MMAs run (two accumulators). No load is multicast. Every wait is
+// next one's MMAs run (two accumulators), warp 3 stores what they stage. No load is multicast. Every wait is
 // bounded, as in gemm_tc_pair.cuh, whose pair protocol this follows.
 //
 // Gated rows. The 32 TMEM lanes of an epilogue warp hold 16 gate and the same
@@ -53,6 +53,7 @@ constexpr int CONV_GROUPS = 2, GROUP_WARPS = 4;
 constexpr int CONV_WARPS = CONV_GROUPS * GROUP_WARPS;
 constexpr int FIRST_CONV = 4, FIRST_EPI = FIRST_CONV + CONV_WARPS;
 constexpr int PAIR_THREADS = 32 * (FIRST_EPI + 4);
+constexpr int BAR_FREE = 2, BAR_STAGED = 4;     // named barriers: a staging set is free / written (two each)
 
 // A stage is 8 MMAs: two sub-tiles of the contraction (128 k, or 64 n, each),
 // or one sub-tile against two planes. (With stages of 4 MMAs the issuing
@@ -94,6 +95,7 @@ struct alignas(1024) PairSmem {
     alignas(16) float tok[NT];    // 1/sx (forward) or the row's power of two
     uint32_t tmem_base;
     int abort;
+    int stop;                     // the epilogue gave up
 };
 
 struct PairArgs {
@@ -154,6 +156,9 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort));
+}
+__device__ __forceinline__ void bar_arrive(int id, int count) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 __device__ __forceinline__ void bulk_wait_read_0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void sts128(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -241,11 +246,28 @@ __device__ __forceinline__ void widen_pieces(const uint4 (&v)[pieces<MODE>()], u
 // half's first row; the saved pre-activations' tiles follow `tile` bytes
 // apart). Every choice is a template argument: branches per element made this
 // loop several times slower.
-__device__ __forceinline__ void sts_elem(uint32_t a, float v, float) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+// (The stores carry no memory clobber: they would order every table load
+// behind them. The barrier that publishes a tile has one.)
+template <int N>
+__device__ __forceinline__ void sts_column(uint32_t a, int row, const float (&v)[N], float) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) asm volatile("st.shared.f32 [%0], %1;" ::"r"(a + j * row), "f"(v[j]));
 }
-__device__ __forceinline__ void sts_elem(uint32_t a, float v, __nv_bfloat16) {
-    asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v))) : "memory");
+template <int N>
+__device__ __forceinline__ void sts_column(uint32_t a, int row, const float (&v)[N], __nv_bfloat16) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2)  // one conversion rounds two values
+        asm volatile(
+            "{\n\t.reg .b16 lo, hi;\n\t.reg .b32 w;\n\tcvt.rn.bf16x2.f32 w, %3, %2;\n\tmov.b32 {lo, hi}, w;\n\t"
+            "st.shared.b16 [%0], lo;\n\tst.shared.b16 [%1], hi;\n\t}" ::"r"(a + j * row),
+            "r"(a + (j + 1) * row), "f"(v[j]), "f"(v[j + 1]));
+}
+__device__ __forceinline__ void load_tokens(float (&t)[16], const float *tok) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 q = reinterpret_cast<const float4 *>(tok)[i];
+        t[4 * i] = q.x; t[4 * i + 1] = q.y; t[4 * i + 2] = q.z; t[4 * i + 3] = q.w;
+    }
 }
 
 template <int ACT, bool GLU, bool SAVE, bool RES, typename T>
@@ -253,36 +275,35 @@ __device__ __forceinline__ void fwd_half(const uint32_t (&v)[16], const float (&
                                          float b, int lane, uint32_t st, int tile) {
     constexpr int ROW = (GLU ? 64 : 128) * (int)sizeof(T);
     float z[16];
+    load_tokens(z, tok);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 t = reinterpret_cast<const float4 *>(tok)[i];
-        z[4 * i] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[4 * i]), t.x), rsw) + b;
-        z[4 * i + 1] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[4 * i + 1]), t.y), rsw) + b;
-        z[4 * i + 2] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[4 * i + 2]), t.z), rsw) + b;
-        z[4 * i + 3] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[4 * i + 3]), t.w), rsw) + b;
-    }
+    for (int j = 0; j < 16; ++j) z[j] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[j]), z[j]), rsw) + b;
     if constexpr (GLU) {
         // lanes 0-15 finish tokens 0-7 of the half, lanes 16-31 tokens 8-15
         const bool gate = lane < 16;
         const uint32_t at = st + (gate ? 0 : 8 * ROW);
+        float g[8], u[8], h[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float got = __shfl_xor_sync(0xffffffffu, gate ? z[8 + j] : z[j], 16);
-            const float g = gate ? z[j] : got, u = gate ? got : z[8 + j];
-            sts_elem(at + j * ROW, act_value<ACT>(g) * u, T());
-            if constexpr (SAVE) {
-                sts_elem(at + j * ROW + tile, g, T());
-                sts_elem(at + j * ROW + 2 * tile, u, T());
-            }
+            g[j] = gate ? z[j] : got;
+            u[j] = gate ? got : z[8 + j];
+            h[j] = act_value<ACT>(g[j]) * u[j];
+        }
+        sts_column(at, ROW, h, T());
+        if constexpr (SAVE) {
+            sts_column(at + tile, ROW, g, T());
+            sts_column(at + 2 * tile, ROW, u, T());
         }
     } else {
+        float y[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-            float y = act_value<ACT>(z[j]);
-            if constexpr (RES) y += r[j];
-            sts_elem(st + j * ROW, y, T());
-            if constexpr (SAVE) sts_elem(st + j * ROW + tile, z[j], T());
+            y[j] = act_value<ACT>(z[j]);
+            if constexpr (RES) y[j] += r[j];
         }
+        sts_column(st, ROW, y, T());
+        if constexpr (SAVE) sts_column(st + tile, ROW, z, T());
     }
 }
 
@@ -348,6 +369,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         }
         ptx::mbar_init(&sm.done, 1);
         sm.abort = 0;
+        sm.stop = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&tm_wa);
         ptx::prefetch_tensormap(&tm_x);
@@ -540,20 +562,22 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                 b = n_ok && bias ? ld_dep(bias + n) : 0.0f;
             }
             // One decision for all four warps (this barrier also publishes the table).
-            if (!ptx::bar_and(1, 128, ptx::mbar_wait(&sm.acc_full[buf], acc_phase, abort))) break;
+            if (!ptx::bar_and(1, 128, ptx::mbar_wait(&sm.acc_full[buf], acc_phase, abort))) {
+                if (p.tma_out) {  // let the store warp leave too
+                    sm.stop = 1;
+                    bar_arrive(BAR_STAGED + sb, 160);
+                }
+                break;
+            }
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int c0 = 0; c0 < NT; c0 += 32) {
                 const int m0 = m_base + c0;
                 if (m0 >= p.M) break;
-                // the staging tiles written below were last read by the stores
-                // of the chunk before last (or of the last one)
-                if (et == 0) {
-                    if (twice) tcp::bulk_wait_read_1();
-                    else bulk_wait_read_0();
-                }
-                ptx::bar_sync(1, 128);
-                uint8_t *stg = sm.epi + (twice ? sb * outs * STG : 0);
+                // the staging tiles are free: the store warp has seen their last
+                // stores read, or the warps themselves have copied them out
+                ptx::bar_sync(p.tma_out ? BAR_FREE + sb : 1, p.tma_out ? 160 : 128);
+                uint8_t *stg = sm.epi + sb * outs * STG;
 #pragma unroll 1
                 for (int h = 0; h < 32; h += 16) {
                     const uint32_t st = ptx::smem_addr(stg) + (uint32_t)((h * COLS + col) * (int)sizeof(T));
@@ -578,27 +602,23 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                         }
 #undef W4A8_HALF
                     } else {
+                        float y[16];
+                        load_tokens(y, tok);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            sts_elem(st + j * COLS * (int)sizeof(T), __uint_as_float(v[j]) * tok[j], T());
+                        for (int j = 0; j < 16; ++j) y[j] *= __uint_as_float(v[j]);
+                        sts_column(st, COLS * (int)sizeof(T), y, T());
                     }
                 }
                 if (p.tma_out) {
                     tcp::fence_proxy_async_smem();  // the staging writes, before the store reads them
-                    ptx::bar_sync(1, 128);
-                    if (et == 0 && n_base < p.N) {
-                        tcp::tma_store_2d(&tm_y, stg, n_base, m0);
-                        if (outs > 1) tcp::tma_store_2d(&tm_z, stg + STG, n_base, m0);
-                        if (outs > 2) tcp::tma_store_2d(&tm_u, stg + 2 * STG, n_base, m0);
-                        tcp::bulk_commit_group();
-                    }
+                    bar_arrive(BAR_STAGED + sb, 160);
                 } else {
                     ptx::bar_sync(1, 128);
                     copy_out<COLS, T>(stg, p.e.Y, p.e.ldy, m0, p.M, n_base, p.N, et);
                     if (outs > 1) copy_out<COLS, T>(stg + STG, p.e.Z, p.e.ldz, m0, p.M, n_base, p.N, et);
                     if (outs > 2) copy_out<COLS, T>(stg + 2 * STG, p.e.U, p.e.ldz, m0, p.M, n_base, p.N, et);
                 }
-                sb ^= 1;
+                if (twice) sb ^= 1;
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -606,8 +626,48 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }
             ptx::bar_sync(1, 128);  // the table is rewritten next tile
         }
+    } else if (warp == 3 && p.tma_out) {
+        // ---------------------------------------------------- output stores
+        // Its own warp, so that neither the store's issue nor the wait for the
+        // staging tiles to be read holds the epilogue up.
+        constexpr int COLS = GLU ? 64 : 128;
+        constexpr int STG = 32 * COLS * (int)sizeof(T);
+        const int outs = 1 + (FWD && p.e.Z ? (GLU ? 2 : 1) : 0);
+        const bool twice = 2 * outs * STG <= EPI_SMEM;
+        int sb = 0;
+        bool first = true;  // the second set of tiles starts free
+        bar_arrive(BAR_FREE, 160);
+        if (twice) bar_arrive(BAR_FREE + 1, 160);
+        bool stop = false;
+        for (int tile = pair; tile < num_tiles && !stop; tile += npairs) {
+            const int n_base = (tile / tiles_m) * TILE_ROWS + rank * COLS, m_base = (tile % tiles_m) * NT;
+            for (int m0 = m_base; m0 < min(m_base + NT, p.M); m0 += 32) {
+                ptx::bar_sync(BAR_STAGED + sb, 160);
+                stop = sm.stop != 0;
+                if (stop) break;
+                if (lane == 0 && n_base < p.N) {
+                    const uint8_t *stg = sm.epi + sb * outs * STG;
+                    tcp::tma_store_2d(&tm_y, stg, n_base, m0);
+                    if (outs > 1) tcp::tma_store_2d(&tm_z, stg + STG, n_base, m0);
+                    if (outs > 2) tcp::tma_store_2d(&tm_u, stg + 2 * STG, n_base, m0);
+                    tcp::bulk_commit_group();
+                }
+                // with two sets of tiles the other set's stores have been read
+                // once at most this group is pending
+                if (twice) {
+                    if (lane == 0) tcp::bulk_wait_read_1();
+                    sb ^= 1;
+                } else if (lane == 0) {
+                    bulk_wait_read_0();
+                }
+                __syncwarp();
+                if (twice && !first) bar_arrive(BAR_FREE + sb, 160);
+                if (!twice) bar_arrive(BAR_FREE, 160);
+                first = false;
+            }
+        }
         // the output stores have completed before the CTA exits
-        if (et == 0 && p.tma_out) tcp::bulk_wait_all();
+        if (lane == 0) tcp::bulk_wait_all();
     }
 
     // Every MMA of the pair has finished before TMEM is released.
