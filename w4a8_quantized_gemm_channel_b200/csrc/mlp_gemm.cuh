@@ -27,14 +27,14 @@
 // Per CTA: 128 rows of A and half of the tile's tokens. Three rings: packed
 // weights and tokens (TMA, freed by the widening and by the MMAs), widened
 // weights. Warp 0 loads weights, warp 2 tokens, warp 1 issues the MMAs (in the
-// leader), warps 4-11 widen, warps 12-15 run the epilogue of one tile while the
+// leader), warps 4-11 widen, warps 12-19 run the epilogue of one tile while the
 // next one's MMAs run (two accumulators), warp 3 stores what they stage. No load is multicast. Every wait is
 // bounded, as in gemm_tc_pair.cuh, whose pair protocol this follows.
 //
 // Gated rows. The 32 TMEM lanes of an epilogue warp hold 16 gate and the same
 // 16 up channels (the widening warps place the rows so), and one shuffle per
-// two outputs brings a channel's pair together: lanes 0-15 finish the chunk's
-// first 16 tokens, lanes 16-31 the others.
+// two outputs brings a channel's pair together: lanes 0-15 finish a unit's first
+// 8 tokens, lanes 16-31 the others.
 #pragma once
 
 #include "gemm_tc_pair.cuh"
@@ -52,8 +52,11 @@ constexpr int EPI_SMEM = 32768;                // output staging
 constexpr int CONV_GROUPS = 2, GROUP_WARPS = 4;
 constexpr int CONV_WARPS = CONV_GROUPS * GROUP_WARPS;
 constexpr int FIRST_CONV = 4, FIRST_EPI = FIRST_CONV + CONV_WARPS;
-constexpr int PAIR_THREADS = 32 * (FIRST_EPI + 4);
-constexpr int BAR_FREE = 2, BAR_STAGED = 4;     // named barriers: a staging set is free / written (two each)
+constexpr int EPI_GROUPS = 2;                  // warpgroups of the epilogue, units in turn
+constexpr int UNIT = 16;                       // tokens of an epilogue unit
+constexpr int PAIR_THREADS = 32 * (FIRST_EPI + 4 * EPI_GROUPS);
+// named barriers: all epilogue warps; a group; a group's staging set free, written
+constexpr int BAR_EPI = 1, BAR_GROUP = 2, BAR_FREE = 4, BAR_STAGED = 8;
 
 // A stage is 8 MMAs: two sub-tiles of the contraction (128 k, or 64 n, each),
 // or one sub-tile against two planes. (With stages of 4 MMAs the issuing
@@ -90,7 +93,7 @@ struct alignas(1024) PairSmem {
     uint64_t empty[S::B_SLOTS];   // MMAs of the stage finished (both CTAs)
     uint64_t ready[S::A_SLOTS];   // leader: both CTAs' operands there (16 warps)
     uint64_t acc_full[2];         // accumulator ready (both CTAs)
-    uint64_t acc_empty[2];        // leader: both CTAs' epilogues drained (8 warps)
+    uint64_t acc_empty[2];        // leader: both CTAs' epilogues drained (16 warps)
     uint64_t done;                // every MMA finished (both CTAs)
     alignas(16) float tok[NT];    // 1/sx (forward) or the row's power of two
     uint32_t tmem_base;
@@ -241,10 +244,9 @@ __device__ __forceinline__ void widen_pieces(const uint4 (&v)[pieces<MODE>()], u
 }
 
 // ---------------------------------------------------------------- epilogue ---
-// Half a chunk (16 tokens) of one TMEM lane, written to the staging tiles
-// [32][COLS] of T at `st` (shared address of this thread's column in the
-// half's first row; the saved pre-activations' tiles follow `tile` bytes
-// apart). Every choice is a template argument: branches per element made this
+// A unit (16 tokens) of one TMEM lane, written to the staging tiles [16][COLS]
+// of T at `st` (shared address of this thread's column in the first row; the
+// saved pre-activations' tiles follow `tile` bytes apart). Every choice is a template argument: branches per element made this
 // loop several times slower.
 // (The stores carry no memory clobber: they would order every table load
 // behind them. The barrier that publishes a tile has one.)
@@ -271,7 +273,7 @@ __device__ __forceinline__ void load_tokens(float (&t)[16], const float *tok) {
 }
 
 template <int ACT, bool GLU, bool SAVE, bool RES, typename T>
-__device__ __forceinline__ void fwd_half(const uint32_t (&v)[16], const float (&r)[16], const float *tok, float rsw,
+__device__ __forceinline__ void fwd_unit(const uint32_t (&v)[16], const float (&r)[16], const float *tok, float rsw,
                                          float b, int lane, uint32_t st, int tile) {
     constexpr int ROW = (GLU ? 64 : 128) * (int)sizeof(T);
     float z[16];
@@ -279,7 +281,7 @@ __device__ __forceinline__ void fwd_half(const uint32_t (&v)[16], const float (&
 #pragma unroll
     for (int j = 0; j < 16; ++j) z[j] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[j]), z[j]), rsw) + b;
     if constexpr (GLU) {
-        // lanes 0-15 finish tokens 0-7 of the half, lanes 16-31 tokens 8-15
+        // lanes 0-15 finish tokens 0-7 of the unit, lanes 16-31 tokens 8-15
         const bool gate = lane < 16;
         const uint32_t at = st + (gate ? 0 : 8 * ROW);
         float g[8], u[8], h[8];
@@ -308,28 +310,45 @@ __device__ __forceinline__ void fwd_half(const uint32_t (&v)[16], const float (&
 }
 
 template <int ACT, bool GLU, typename T>
-__device__ __forceinline__ void fwd_half_any(bool save, bool res, const uint32_t (&v)[16], const float (&r)[16],
+__device__ __forceinline__ void fwd_unit_any(bool save, bool res, const uint32_t (&v)[16], const float (&r)[16],
                                              const float *tok, float rsw, float b, int lane, uint32_t st, int tile) {
     if (GLU || !res) {
-        if (save) fwd_half<ACT, GLU, true, false, T>(v, r, tok, rsw, b, lane, st, tile);
-        else fwd_half<ACT, GLU, false, false, T>(v, r, tok, rsw, b, lane, st, tile);
+        if (save) fwd_unit<ACT, GLU, true, false, T>(v, r, tok, rsw, b, lane, st, tile);
+        else fwd_unit<ACT, GLU, false, false, T>(v, r, tok, rsw, b, lane, st, tile);
     } else {
-        if (save) fwd_half<ACT, GLU, true, true, T>(v, r, tok, rsw, b, lane, st, tile);
-        else fwd_half<ACT, GLU, false, true, T>(v, r, tok, rsw, b, lane, st, tile);
+        if (save) fwd_unit<ACT, GLU, true, true, T>(v, r, tok, rsw, b, lane, st, tile);
+        else fwd_unit<ACT, GLU, false, true, T>(v, r, tok, rsw, b, lane, st, tile);
     }
 }
 
-// A staged chunk to memory by the four warps, where the arrays' alignment
-// does not allow the TMA store.
+// A staged unit to memory by a group's four warps, where the arrays'
+// alignment does not allow the TMA store.
 template <int COLS, typename T>
 __device__ __forceinline__ void copy_out(const uint8_t *stg, void *out, int ld, int m0, int M, int n0, int N, int et) {
     const T *s = reinterpret_cast<const T *>(stg);
-    const int rows = min(32, M - m0);
+    const int rows = min(UNIT, M - m0);
     for (int i = et; i < rows * COLS; i += 128) {
         const int r = i / COLS, c = i % COLS;
         if (n0 + c < N) static_cast<T *>(out)[(size_t)(m0 + r) * ld + n0 + c] = s[i];
     }
 }
+
+// Staging of a call: each group owns half of EPI_SMEM, one or two sets of tiles.
+template <int MODE, typename T>
+struct Staging {
+    static constexpr int COLS = MODE == FWD_GLU ? 64 : 128;
+    static constexpr int TILE = UNIT * COLS * (int)sizeof(T);
+    int outs, sets;
+    __device__ __forceinline__ explicit Staging(const EpiArgs &e) {
+        outs = 1 + ((MODE == FWD_LINEAR || MODE == FWD_GLU) && e.Z ? (MODE == FWD_GLU ? 2 : 1) : 0);
+        sets = 2 * outs * TILE * EPI_GROUPS <= EPI_SMEM ? 2 : 1;
+    }
+    __device__ __forceinline__ uint8_t *at(uint8_t *epi, int group, int set) const {
+        return epi + group * (EPI_SMEM / EPI_GROUPS) + set * outs * TILE;
+    }
+};
+static_assert(Staging<FWD_LINEAR, float>::TILE * 2 * EPI_GROUPS <= EPI_SMEM &&
+              Staging<FWD_GLU, float>::TILE * 3 * EPI_GROUPS <= EPI_SMEM, "one set of every call fits");
 
 template <int MODE, int NT, typename T>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
@@ -365,7 +384,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         for (int a = 0; a < A_SLOTS; ++a) ptx::mbar_init(&sm.ready[a], 2 * CONV_WARPS);
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&sm.acc_full[b], 1);
-            ptx::mbar_init(&sm.acc_empty[b], 8);
+            ptx::mbar_init(&sm.acc_empty[b], 2 * 4 * EPI_GROUPS);
         }
         ptx::mbar_init(&sm.done, 1);
         sm.abort = 0;
@@ -533,26 +552,27 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         }
     } else if (warp >= FIRST_EPI) {
         // ---------------------------------------------------- epilogue (each CTA: its 128 TMEM lanes)
-        const int q = warp & 3, et = threadIdx.x - 32 * FIRST_EPI;
-        constexpr int COLS = GLU ? 64 : 128;
+        // Two groups of four warps (one per quarter of the lanes) take units of
+        // 16 tokens in turn.
+        const int q = warp & 3, eg = (warp - FIRST_EPI) >> 2;
+        const int ea = threadIdx.x - 32 * FIRST_EPI, et = ea & 127;
+        const Staging<MODE, T> sg(p.e);
+        constexpr int COLS = sg.COLS, TILE = sg.TILE;
         // this thread's output column inside the CTA's COLS (the gradient's
         // rows come in the order of the widening masks)
         const int col = GLU ? 16 * q + (lane & 15)
                             : FWD ? et : (et & ~7) | ((et & 7) >> 1) | ((et & 1) << 2);
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-        const int outs = 1 + (FWD && p.e.Z ? (GLU ? 2 : 1) : 0);
-        constexpr int STG = 32 * COLS * (int)sizeof(T);  // bytes of a staging tile
-        const bool twice = 2 * outs * STG <= EPI_SMEM;
         const bool res = FWD && !GLU && p.e.R != nullptr;
-        int buf = 0, sb = 0;
+        int buf = 0, set = 0;
         uint32_t acc_phase = 0;
         for (int tile = pair; tile < num_tiles; tile += npairs) {
             const int n_tile = tile / tiles_m, m_base = (tile % tiles_m) * NT;
             const int n_base = n_tile * TILE_ROWS + rank * COLS, n = n_base + col;
             const bool n_ok = n < p.N;
-            for (int c = et; c < NT; c += 128) {
-                const float t = m_base + c < p.M ? ld_dep(p.tok + m_base + c) : 1.0f;
-                sm.tok[c] = FWD ? __frcp_rn(t) : t;
+            if (ea < NT) {
+                const float t = m_base + ea < p.M ? ld_dep(p.tok + m_base + ea) : 1.0f;
+                sm.tok[ea] = FWD ? __frcp_rn(t) : t;
             }
             float rsw = 1.0f, b = 0.0f;
             if constexpr (FWD) {
@@ -561,109 +581,105 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                 rsw = n_ok ? __frcp_rn(ld_dep(sw + n)) * 0.0625f : 1.0f;  // the accumulator holds 16 x the sum
                 b = n_ok && bias ? ld_dep(bias + n) : 0.0f;
             }
-            // One decision for all four warps (this barrier also publishes the table).
-            if (!ptx::bar_and(1, 128, ptx::mbar_wait(&sm.acc_full[buf], acc_phase, abort))) {
+            // One decision for all warps (this barrier also publishes the table).
+            if (!ptx::bar_and(BAR_EPI, 128 * EPI_GROUPS, ptx::mbar_wait(&sm.acc_full[buf], acc_phase, abort))) {
                 if (p.tma_out) {  // let the store warp leave too
                     sm.stop = 1;
-                    bar_arrive(BAR_STAGED + sb, 160);
+                    bar_arrive(BAR_STAGED + 2 * eg + set, 160);
                 }
                 break;
             }
             ptx::tc_fence_after();
 #pragma unroll 1
-            for (int c0 = 0; c0 < NT; c0 += 32) {
+            for (int c0 = UNIT * eg; c0 < NT; c0 += UNIT * EPI_GROUPS) {
                 const int m0 = m_base + c0;
                 if (m0 >= p.M) break;
                 // the staging tiles are free: the store warp has seen their last
-                // stores read, or the warps themselves have copied them out
-                ptx::bar_sync(p.tma_out ? BAR_FREE + sb : 1, p.tma_out ? 160 : 128);
-                uint8_t *stg = sm.epi + sb * outs * STG;
-#pragma unroll 1
-                for (int h = 0; h < 32; h += 16) {
-                    const uint32_t st = ptx::smem_addr(stg) + (uint32_t)((h * COLS + col) * (int)sizeof(T));
-                    uint32_t v[16];
-                    float r[16];
-                    if (res) {  // indexes past the edges repeat the last row or column
-                        const T *R = static_cast<const T *>(p.e.R) + min(n, p.N - 1);
+                // stores read, or the group itself has copied them out
+                if (p.tma_out) ptx::bar_sync(BAR_FREE + 2 * eg + set, 160);
+                else ptx::bar_sync(BAR_GROUP + eg, 128);
+                uint8_t *stg = sg.at(sm.epi, eg, set);
+                const uint32_t st = ptx::smem_addr(stg) + (uint32_t)(col * (int)sizeof(T));
+                uint32_t v[16];
+                float r[16];
+                if (res) {  // indexes past the edges repeat the last row or column
+                    const T *R = static_cast<const T *>(p.e.R) + min(n, p.N - 1);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) r[j] = ld_elem(R + (size_t)min(m0 + h + j, p.M - 1) * p.e.ldr);
+                    for (int j = 0; j < 16; ++j) r[j] = ld_elem(R + (size_t)min(m0 + j, p.M - 1) * p.e.ldr);
+                }
+                ptx::tmem_ld_32x32b_x16(tmem + lane_base + (uint32_t)(buf * 256 + c0), v);
+                ptx::tmem_wait_ld();
+                const float *tok = sm.tok + c0;
+                if constexpr (FWD) {
+#define W4A8_UNIT(A) fwd_unit_any<A, GLU, T>(p.e.Z != nullptr, res, v, r, tok, rsw, b, lane, st, TILE)
+                    switch (p.act) {
+                        case W4A8_ACT_NONE: W4A8_UNIT(W4A8_ACT_NONE); break;
+                        case W4A8_ACT_RELU: W4A8_UNIT(W4A8_ACT_RELU); break;
+                        case W4A8_ACT_SILU: W4A8_UNIT(W4A8_ACT_SILU); break;
+                        case W4A8_ACT_GELU: W4A8_UNIT(W4A8_ACT_GELU); break;
+                        default: W4A8_UNIT(W4A8_ACT_GELU_TANH); break;
                     }
-                    ptx::tmem_ld_32x32b_x16(tmem + lane_base + (uint32_t)(buf * 256 + c0 + h), v);
-                    ptx::tmem_wait_ld();
-                    const float *tok = sm.tok + c0 + h;
-                    if constexpr (FWD) {
-#define W4A8_HALF(A) fwd_half_any<A, GLU, T>(p.e.Z != nullptr, res, v, r, tok, rsw, b, lane, st, STG)
-                        switch (p.act) {
-                            case W4A8_ACT_NONE: W4A8_HALF(W4A8_ACT_NONE); break;
-                            case W4A8_ACT_RELU: W4A8_HALF(W4A8_ACT_RELU); break;
-                            case W4A8_ACT_SILU: W4A8_HALF(W4A8_ACT_SILU); break;
-                            case W4A8_ACT_GELU: W4A8_HALF(W4A8_ACT_GELU); break;
-                            default: W4A8_HALF(W4A8_ACT_GELU_TANH); break;
-                        }
-#undef W4A8_HALF
-                    } else {
-                        float y[16];
-                        load_tokens(y, tok);
+#undef W4A8_UNIT
+                } else {
+                    float y[16];
+                    load_tokens(y, tok);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) y[j] *= __uint_as_float(v[j]);
-                        sts_column(st, COLS * (int)sizeof(T), y, T());
-                    }
+                    for (int j = 0; j < 16; ++j) y[j] *= __uint_as_float(v[j]);
+                    sts_column(st, COLS * (int)sizeof(T), y, T());
                 }
                 if (p.tma_out) {
                     tcp::fence_proxy_async_smem();  // the staging writes, before the store reads them
-                    bar_arrive(BAR_STAGED + sb, 160);
+                    bar_arrive(BAR_STAGED + 2 * eg + set, 160);
                 } else {
-                    ptx::bar_sync(1, 128);
+                    ptx::bar_sync(BAR_GROUP + eg, 128);
                     copy_out<COLS, T>(stg, p.e.Y, p.e.ldy, m0, p.M, n_base, p.N, et);
-                    if (outs > 1) copy_out<COLS, T>(stg + STG, p.e.Z, p.e.ldz, m0, p.M, n_base, p.N, et);
-                    if (outs > 2) copy_out<COLS, T>(stg + 2 * STG, p.e.U, p.e.ldz, m0, p.M, n_base, p.N, et);
+                    if (sg.outs > 1) copy_out<COLS, T>(stg + TILE, p.e.Z, p.e.ldz, m0, p.M, n_base, p.N, et);
+                    if (sg.outs > 2) copy_out<COLS, T>(stg + 2 * TILE, p.e.U, p.e.ldz, m0, p.M, n_base, p.N, et);
                 }
-                if (twice) sb ^= 1;
+                if (sg.sets == 2) set ^= 1;
             }
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) tcp::mbar_arrive_leader(&sm.acc_empty[buf]);
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }
-            ptx::bar_sync(1, 128);  // the table is rewritten next tile
+            ptx::bar_sync(BAR_EPI, 128 * EPI_GROUPS);  // the table is rewritten next tile
         }
     } else if (warp == 3 && p.tma_out) {
         // ---------------------------------------------------- output stores
         // Its own warp, so that neither the store's issue nor the wait for the
-        // staging tiles to be read holds the epilogue up.
-        constexpr int COLS = GLU ? 64 : 128;
-        constexpr int STG = 32 * COLS * (int)sizeof(T);
-        const int outs = 1 + (FWD && p.e.Z ? (GLU ? 2 : 1) : 0);
-        const bool twice = 2 * outs * STG <= EPI_SMEM;
-        int sb = 0;
-        bool first = true;  // the second set of tiles starts free
-        bar_arrive(BAR_FREE, 160);
-        if (twice) bar_arrive(BAR_FREE + 1, 160);
+        // staging tiles to be read holds the epilogue up. Units in order: the
+        // groups in turn, each group's sets in turn.
+        const Staging<MODE, T> sg(p.e);
+        constexpr int COLS = sg.COLS, TILE = sg.TILE;
+        int unit[EPI_GROUPS] = {};  // units each group has had
+        for (int i = 0; i < EPI_GROUPS * sg.sets; ++i) bar_arrive(BAR_FREE + 2 * (i % EPI_GROUPS) + i / EPI_GROUPS, 160);
         bool stop = false;
         for (int tile = pair; tile < num_tiles && !stop; tile += npairs) {
             const int n_base = (tile / tiles_m) * TILE_ROWS + rank * COLS, m_base = (tile % tiles_m) * NT;
-            for (int m0 = m_base; m0 < min(m_base + NT, p.M); m0 += 32) {
-                ptx::bar_sync(BAR_STAGED + sb, 160);
+            const int units = (min(NT, p.M - m_base) + UNIT - 1) / UNIT;
+            for (int i = 0; i < units; ++i) {
+                const int eg = i % EPI_GROUPS, m0 = m_base + i * UNIT;
+                const int set = sg.sets == 2 ? unit[eg] & 1 : 0;
+                ptx::bar_sync(BAR_STAGED + 2 * eg + set, 160);
                 stop = sm.stop != 0;
                 if (stop) break;
-                if (lane == 0 && n_base < p.N) {
-                    const uint8_t *stg = sm.epi + sb * outs * STG;
-                    tcp::tma_store_2d(&tm_y, stg, n_base, m0);
-                    if (outs > 1) tcp::tma_store_2d(&tm_z, stg + STG, n_base, m0);
-                    if (outs > 2) tcp::tma_store_2d(&tm_u, stg + 2 * STG, n_base, m0);
+                if (lane == 0) {
+                    const uint8_t *stg = sg.at(sm.epi, eg, set);
+                    if (n_base < p.N) {
+                        tcp::tma_store_2d(&tm_y, stg, n_base, m0);
+                        if (sg.outs > 1) tcp::tma_store_2d(&tm_z, stg + TILE, n_base, m0);
+                        if (sg.outs > 2) tcp::tma_store_2d(&tm_u, stg + 2 * TILE, n_base, m0);
+                    }
                     tcp::bulk_commit_group();
-                }
-                // with two sets of tiles the other set's stores have been read
-                // once at most this group is pending
-                if (twice) {
-                    if (lane == 0) tcp::bulk_wait_read_1();
-                    sb ^= 1;
-                } else if (lane == 0) {
-                    bulk_wait_read_0();
+                    // one set: this unit has been read; two: every earlier one
+                    if (sg.sets == 2) tcp::bulk_wait_read_1();
+                    else bulk_wait_read_0();
                 }
                 __syncwarp();
-                if (twice && !first) bar_arrive(BAR_FREE + sb, 160);
-                if (!twice) bar_arrive(BAR_FREE, 160);
-                first = false;
+                // so the group's only set, or the one of its previous unit, is free
+                if (sg.sets == 1) bar_arrive(BAR_FREE + 2 * eg, 160);
+                else if (unit[eg] > 0) bar_arrive(BAR_FREE + 2 * eg + (set ^ 1), 160);
+                ++unit[eg];
             }
         }
         // the output stores have completed before the CTA exits
@@ -731,7 +747,7 @@ w4a8_status launch_pair(PairArgs p, const PairCall &c, cudaStream_t stream) {
     for (int i = 0; i < 3 && tma; ++i)
         if (arr[i])
             tma = tc::make_map_2d(&out[i], t, arr[i], (uint64_t)p.N, (uint64_t)p.M, (uint64_t)ld[i] * sizeof(T), COLS,
-                                  32, CU_TENSOR_MAP_SWIZZLE_NONE);
+                                  UNIT, CU_TENSOR_MAP_SWIZZLE_NONE);
     p.tma_out = tma;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(PAIR_THREADS);
