@@ -4,6 +4,7 @@
 #pragma once
 
 #include "mlp_gemm.cuh"
+#include "mlp_decode.cuh"
 
 namespace w4a8 {
 namespace {
@@ -63,27 +64,41 @@ w4a8_status launch_quant_rows(const void *X, int M, int K, int ldx, const Worksp
     return from_cuda(e);
 }
 
-// The kernel path of a call: the forced one, else by size. A few thousand
-// products per SM do not fill a tensor-core tile's pipeline.
-unsigned mlp_path(int M, int K, int N, int segs, unsigned flags) {
-    const unsigned forced = flags & W4A8_PATH_MASK;
-    if (forced) return forced;
-    return (double)M * N * K * segs < 65536.0 ? W4A8_PATH_GENERIC : W4A8_PATH_TC;
-}
+// Few products: the CUDA-core form, whose launch is the cheapest.
+bool mlp_tiny(int M, int K, int N, int segs) { return (double)M * N * K * segs < 65536.0; }
 
 template <bool GLU, typename T>
 w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a, const mlp::Proj &b, int ldp, int N,
                         int act, const mlp::EpiArgs &ea, unsigned flags, const Workspace &ws, cudaStream_t s) {
-    const unsigned path = mlp_path(M, K, N, GLU ? 2 : 1, flags);
-    if (path != W4A8_PATH_GENERIC && path != W4A8_PATH_TC) return W4A8_ERR_UNSUPPORTED;
-    if (path == W4A8_PATH_TC && tc::encode_fn() == nullptr) return W4A8_ERR_UNSUPPORTED;
-    w4a8_status st = launch_quant_rows<T>(X, M, K, ldx, ws, flags, s);
+    const int sms = device_info().sm_count;
+    const bool early = (flags & W4A8_STATIC_WEIGHTS) != 0;
+    unsigned path = flags & W4A8_PATH_MASK;
+    const mlp::DecPlan dec = mlp::dec_plan(M, K, N, GLU ? 8 : 16, sms);
+    if (path == W4A8_PATH_AUTO)
+        path = mlp_tiny(M, K, N, GLU ? 2 : 1) ? W4A8_PATH_GENERIC : dec.ok ? W4A8_PATH_DECODE : W4A8_PATH_TC;
+    if (path != W4A8_PATH_GENERIC && path != W4A8_PATH_DECODE && path != W4A8_PATH_TC) return W4A8_ERR_UNSUPPORTED;
+    if (path == W4A8_PATH_DECODE && !dec.ok) return W4A8_ERR_UNSUPPORTED;
+    if (path != W4A8_PATH_GENERIC && tc::encode_fn() == nullptr) return W4A8_ERR_UNSUPPORTED;
+    const bool fused = path == W4A8_PATH_DECODE && dec.units > 0;
+    w4a8_status st = W4A8_OK;
+    if (!fused) st = launch_quant_rows<T>(X, M, K, ldx, ws, flags, s);
     if (st != W4A8_OK) return st;
+    if (path == W4A8_PATH_DECODE) {
+        // behind the row pass the weights are settled: it lets dependents
+        // start only once all earlier work has completed
+        const mlp::DecArgs p = {X, ws.xq, ws.sx, ldx, ws.ldq, io_vec(X, ldx, flags), M, K, N, a, b, ea, act, 0,
+                                early || !fused};
+        st = mlp::launch_decode_any<GLU, T>(dec, p, ldp, s);
+        if (st != W4A8_OK) return st;
+        t_last_path = W4A8_PATH_DECODE;
+        t_last_launches = fused ? 1 : 2;
+        t_last_kernel = "k_mlp_decode";
+        return W4A8_OK;
+    }
     if (path == W4A8_PATH_TC) {
         const int stages = (K + 255) / 256;
-        const mlp::PairArgs p = {M, N, K, stages, stages, ws.sx, a, b, ea, act, 0,
-                                 (flags & W4A8_STATIC_WEIGHTS) != 0};
-        const mlp::PairCall c = {a.Wp, b.Wp, N, ldp, ws.xq, M, ws.ldq, device_info().sm_count};
+        const mlp::PairArgs p = {M, N, K, stages, stages, ws.sx, a, b, ea, act, 0, 1};
+        const mlp::PairCall c = {a.Wp, b.Wp, N, ldp, ws.xq, M, ws.ldq, sms};
         st = mlp::launch_pair_any<GLU ? mlp::FWD_GLU : mlp::FWD_LINEAR, T>(p, c, s);
         if (st != W4A8_OK) return st;
         t_last_path = W4A8_PATH_TC;
@@ -152,7 +167,8 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
     constexpr int SEGS = GLU ? 2 : 1;
     constexpr bool LO = std::is_same<T, float>::value;
     const int N = in.N;
-    const unsigned path = mlp_path(M, K, N, SEGS, flags);
+    unsigned path = flags & W4A8_PATH_MASK;
+    if (path == W4A8_PATH_AUTO) path = mlp_tiny(M, K, N, SEGS) ? W4A8_PATH_GENERIC : W4A8_PATH_TC;
     if (path != W4A8_PATH_GENERIC && path != W4A8_PATH_TC) return W4A8_ERR_UNSUPPORTED;
     if (path == W4A8_PATH_TC && tc::encode_fn() == nullptr) return W4A8_ERR_UNSUPPORTED;
     unsigned launches = 0;

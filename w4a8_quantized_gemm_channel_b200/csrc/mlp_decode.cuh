@@ -1,0 +1,329 @@
+// Few-row form of the MLP operators' forward calls (M <= 16): the packed
+// weights stream once through shared memory, everything else happens beside
+// the stream.
+//
+// Bound: HBM, N K / 2 bytes per projection. The block is that of k_decode_ring
+// (decode_bulk.cuh): one producer thread keeps a ring of TMA stages full (16
+// packed rows x up to 2 KB each), 8 consumer warps multiply a stage with the
+// INT8 rows on the legacy integer tensor-core path, 16 q nibbles, K <= 131072.
+//
+// Gated form: a stage holds 8 gate rows and the same 8 up rows, so that the
+// m16n8k32 product leaves a channel's two projections in one thread's
+// accumulators and one thread finishes act(g) u; nothing is exchanged beyond
+// the sum over the warps.
+//
+// The INT8 rows come from the row pass, or (FUSED, few values) from X itself:
+// every block quantizes all rows, the values held in registers between the
+// abs-max and the codes, which saves the launch of the row pass. Rows sit in
+// shared memory in the k-permuted order of the nibble masks.
+#pragma once
+
+#include "decode_bulk.cuh"
+#include "mlp_act.cuh"
+#include "mlp_simt.cuh"
+
+namespace w4a8 {
+namespace mlp {
+
+constexpr int DEC_TOK = 16;                 // rows at most
+constexpr int DEC_RING = 12;                // ring slots at most
+constexpr int DEC_THREADS = dbulk::THREADS; // 8 consumer warps and the producer
+constexpr int DEC_CONSUMERS = dbulk::CONSUMERS;
+
+struct DecArgs {
+    const void *X;       // FUSED: rows of T
+    const int8_t *Xq;    // else: INT8 rows (permuted order) and scales
+    const float *sx;
+    int ldx, ldq, vec;
+    int M, K, N;
+    Proj a, b;
+    EpiArgs e;
+    int act, ring, early;
+};
+
+struct DecSmem {
+    uint64_t full[DEC_RING], empty[DEC_RING];
+    float part[dbulk::CONSUMER_WARPS];
+    float rsx[DEC_TOK];
+    int32_t red[dbulk::CONSUMER_WARPS][16][DEC_TOK + 1];
+    int abort;
+};
+
+constexpr int DEC_DYN_SMEM = dbulk::SM_SMEM - (int)sizeof(DecSmem) - 1024;  // what a block may ask for
+
+// Quantize row r of X (J units of 8 values per thread) into xs.
+template <int J, typename T>
+__device__ __forceinline__ void dec_quantize(const DecArgs &p, int r, int ks, int8_t *xs, DecSmem &sm, int tid) {
+    float v[J][8], a = 0.0f;
+    const T *x = static_cast<const T *>(p.X) + (size_t)r * p.ldx;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int k = 8 * (tid + DEC_CONSUMERS * j);
+        ld_row8(x, k, p.K, p.vec != 0, v[j]);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) a = fmaxf(a, fabsf(v[j][b]));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if ((tid & 31) == 0) sm.part[tid >> 5] = a;
+    ptx::bar_sync(1, DEC_CONSUMERS);
+    a = sm.part[0];
+#pragma unroll
+    for (int w = 1; w < dbulk::CONSUMER_WARPS; ++w) a = fmaxf(a, sm.part[w]);
+    ptx::bar_sync(1, DEC_CONSUMERS);  // part is rewritten by the next row
+    const float s = act_scale_from_amax(a);
+    if (tid == 0) sm.rsx[r] = __frcp_rn(s);
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int k = 8 * (tid + DEC_CONSUMERS * j);
+        if (k < ks) *reinterpret_cast<uint2 *>(xs + k) = dbulk::act_codes8_perm(v[j], s, k, p.K);
+    }
+}
+
+// MMAs of one stage for NTG groups of 8 rows: chunks of 64 packed bytes (128 k)
+// warp, warp + 8, ...; xs: the INT8 rows, pitch bytes apart, at the stage's k.
+template <int NTG>
+__device__ __forceinline__ void dec_stage(int32_t (&acc)[NTG][2][4], const uint8_t *st, int sb, const int8_t *xs,
+                                          int pitch, int M, int g, int t, int warp) {
+    const int cps = sb / 64;
+#pragma unroll 2
+    for (int c = warp; c < cps; c += dbulk::CONSUMER_WARPS) {
+        const uint4 wa = ptx::lds128(st + g * sb + 64 * c + 16 * t);
+        const uint4 wb = ptx::lds128(st + (g + 8) * sb + 64 * c + 16 * t);
+        const uint32_t pa[4] = {wa.x, wa.y, wa.z, wa.w}, pb[4] = {wb.x, wb.y, wb.z, wb.w};
+        uint4 x[NTG][2];
+#pragma unroll
+        for (int i = 0; i < NTG; ++i) {
+            const int8_t *xp = xs + (size_t)(8 * i + g) * pitch + 128 * c + 32 * t;
+            const bool ok = 8 * i + g < M;
+            x[i][0] = ok ? ptx::lds128(xp) : make_uint4(0, 0, 0, 0);
+            x[i][1] = ok ? ptx::lds128(xp + 16) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            constexpr uint32_t H = 0xF0F0F0F0u;
+            const uint32_t alo = (pa[j] << 4) & H, ahi = pa[j] & H, blo = (pb[j] << 4) & H, bhi = pb[j] & H;
+#pragma unroll
+            for (int i = 0; i < NTG; ++i) {
+                const uint4 &v = x[i][j >> 1];
+                mma_s8_16832(acc[i][j & 1], alo, blo, ahi, bhi, (j & 1) ? v.z : v.x, (j & 1) ? v.w : v.y);
+            }
+        }
+    }
+}
+
+// J > 0: FUSED with J units of 8 values per thread and row. J = 0: INT8 rows.
+template <bool GLU, int NTG, int J, typename T>
+__global__ void __launch_bounds__(DEC_THREADS, 2)
+k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const DecArgs p) {
+    constexpr int TOK = 8 * NTG;
+    constexpr int CH = GLU ? 8 : 16;  // channels per group of 16 packed rows
+    __shared__ DecSmem sm;
+    extern __shared__ __align__(1024) uint8_t dyn_smem[];
+    const dbulk::Geometry geo(p.K);
+    const int sb = geo.sb, nst = geo.nst, pitch = geo.pitch, stage_bytes = geo.stage_bytes(), ks = pitch - 16;
+    int8_t *xs = reinterpret_cast<int8_t *>(dyn_smem + (size_t)p.ring * stage_bytes);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int groups = (p.N + CH - 1) / CH;
+    const int my_groups = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    const int items = my_groups * nst;
+    volatile int *abort = &sm.abort;
+
+    if (tid == 0) {
+        for (int s = 0; s < p.ring; ++s) {
+            ptx::mbar_init(&sm.full[s], 1);
+            ptx::mbar_init(&sm.empty[s], dbulk::CONSUMER_WARPS);
+        }
+        sm.abort = 0;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_launch_dependents();
+
+    if (warp == dbulk::CONSUMER_WARPS) {
+        // ------------------------------------------------- producer (lane 0)
+        int issued = 0;
+        auto issue = [&](int it) {
+            const int j = it / nst, s = it - j * nst, slot = it % p.ring;
+            const int n0 = ((int)blockIdx.x + j * (int)gridDim.x) * CH;
+            uint8_t *dst = dyn_smem + (size_t)slot * stage_bytes;
+            ptx::mbar_arrive_expect_tx(&sm.full[slot], (uint32_t)stage_bytes);
+            ptx::tma_load_2d(dst, &tm_a, s * (sb / 8), n0, &sm.full[slot]);
+            if constexpr (GLU) ptx::tma_load_2d(dst + 8 * sb, &tm_b, s * (sb / 8), n0, &sm.full[slot]);
+            ++issued;
+        };
+        const int pre = min(p.ring, items);
+        if (lane == 0) {
+            ptx::prefetch_tensormap(&tm_a);
+            if (p.early)
+                for (int it = 0; it < pre; ++it) issue(it);
+        }
+        __syncwarp();  // a lane waiting in griddepcontrol.wait holds its warp
+        griddep_wait();
+        if (lane != 0) return;
+        for (int it = issued; it < items; ++it) {
+            // a slot is free once every consumer warp arrived on its last use
+            if (it >= p.ring && !ptx::mbar_wait(&sm.empty[it % p.ring], (uint32_t)(it / p.ring - 1) & 1u, abort)) break;
+            issue(it);
+        }
+        // the block may exit only when every copy it issued has landed
+        for (int it = max(0, issued - p.ring); it < issued; ++it)
+            ptx::mbar_wait_drain(&sm.full[it % p.ring], (uint32_t)(it / p.ring) & 1u);
+        return;
+    }
+
+    // -------------------------------------------------------------- consumers
+    const int g = lane >> 2, t = lane & 3;
+    griddep_wait();
+    if constexpr (J > 0) {
+        for (int r = 0; r < p.M; ++r) dec_quantize<J, T>(p, r, ks, xs + (size_t)r * pitch, sm, tid);
+    } else {
+        const int per = ks / 16, have = min(p.ldq, ks) / 16;
+#pragma unroll 4
+        for (int i = tid; i < p.M * per; i += DEC_CONSUMERS) {
+            const int r = i / per, c = i - r * per;
+            *reinterpret_cast<uint4 *>(xs + (size_t)r * pitch + 16 * c) =
+                c < have ? ld_dep_v4(p.Xq + (size_t)r * p.ldq + 16 * c) : make_uint4(0, 0, 0, 0);
+        }
+        if (tid < p.M) sm.rsx[tid] = __frcp_rn(ld_dep(p.sx + tid));
+    }
+    ptx::bar_sync(1, DEC_CONSUMERS);
+
+    // thread e < CH x TOK finishes channel e % CH of row e / CH
+    const int ch = tid % CH, tk = tid / CH;
+    const bool mine = tid < CH * TOK && tk < p.M;
+    const float rx = mine ? sm.rsx[tk] : 0.0f;
+    for (int j = 0; j < my_groups; ++j) {
+        const int n = ((int)blockIdx.x + j * (int)gridDim.x) * CH + ch;
+        const bool ok = mine && n < p.N;
+        // needed after the group's MMAs: the loads overlap them
+        float sa = 1.0f, ba = 0.0f, sc = 1.0f, bb = 0.0f, r = 0.0f;
+        if (ok) {
+            sa = ld_dep(p.a.sw + n);
+            if (p.a.bias) ba = ld_dep(p.a.bias + n);
+            if constexpr (GLU) {
+                sc = ld_dep(p.b.sw + n);
+                if (p.b.bias) bb = ld_dep(p.b.bias + n);
+            } else {
+                if (p.e.R) r = ld_elem(static_cast<const T *>(p.e.R) + (size_t)tk * p.e.ldr + n);
+            }
+        }
+        int32_t acc[NTG][2][4];
+#pragma unroll
+        for (int i = 0; i < NTG; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) acc[i][q][0] = acc[i][q][1] = acc[i][q][2] = acc[i][q][3] = 0;
+        bool alive = true;
+        for (int s = 0; s < nst; ++s) {
+            const int it = j * nst + s, slot = it % p.ring;
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.full[slot], (uint32_t)(it / p.ring) & 1u, abort))) {
+                alive = false;
+                break;
+            }
+            dec_stage<NTG>(acc, dyn_smem + (size_t)slot * stage_bytes, sb, xs + 2 * sb * s, pitch, p.M, g, t, warp);
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sm.empty[slot]);
+        }
+        // the warps' C fragments (rows g, g + 8, columns 2t, 2t + 1) meet in shared memory
+#pragma unroll
+        for (int i = 0; i < NTG; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                sm.red[warp][g + 8 * (q >> 1)][8 * i + 2 * t + (q & 1)] = acc[i][0][q] + acc[i][1][q];
+        if (!ptx::bar_and(1, DEC_CONSUMERS, alive)) {
+            if (tid == 0) *abort = 1;  // lets the producer stop refilling
+            return;
+        }
+        if (ok) {
+            int32_t ca = 0, cb = 0;
+#pragma unroll
+            for (int w = 0; w < dbulk::CONSUMER_WARPS; ++w) {
+                ca += sm.red[w][ch][tk];
+                if constexpr (GLU) cb += sm.red[w][8 + ch][tk];
+            }
+            const float z = dequant(ca, rx, __frcp_rn(sa) * 0.0625f, ba);  // the sums hold 16 x the product
+            const float u = GLU ? dequant(cb, rx, __frcp_rn(sc) * 0.0625f, bb) : 0.0f;
+            float y = z;
+            switch (p.act) {
+                case W4A8_ACT_RELU: y = act_value<W4A8_ACT_RELU>(z); break;
+                case W4A8_ACT_SILU: y = act_value<W4A8_ACT_SILU>(z); break;
+                case W4A8_ACT_GELU: y = act_value<W4A8_ACT_GELU>(z); break;
+                case W4A8_ACT_GELU_TANH: y = act_value<W4A8_ACT_GELU_TANH>(z); break;
+                default: break;
+            }
+            y = GLU ? y * u : p.e.R ? y + r : y;
+            st_elem(static_cast<T *>(p.e.Y) + (size_t)tk * p.e.ldy + n, y);
+            if (p.e.Z) {
+                st_elem(static_cast<T *>(p.e.Z) + (size_t)tk * p.e.ldz + n, z);
+                if constexpr (GLU) st_elem(static_cast<T *>(p.e.U) + (size_t)tk * p.e.ldz + n, u);
+            }
+        }
+        ptx::bar_sync(1, DEC_CONSUMERS);  // red is rewritten by the next group
+    }
+}
+
+// ------------------------------------------------------------- host side ---
+
+struct DecPlan {
+    bool ok;
+    int units;      // FUSED: units of 8 values per thread and row (1, 2, 4, 8), 0: INT8 rows
+    int grid, ring;
+    size_t smem;
+};
+
+// Two blocks per SM share its shared memory where the rows leave each a ring
+// of three stages, one block otherwise. FUSED while all rows are at most eight units of 8 values
+// per thread (2048 values a unit): beyond that every block's pass over X
+// costs more than the row pass's launch.
+inline DecPlan dec_plan(int M, int K, int N, int ch, int sms) {
+    DecPlan d = {};
+    if (M < 1 || M > DEC_TOK || K > dbulk::X16_MAX_K) return d;
+    const dbulk::Geometry geo(K);
+    const long long stage = geo.stage_bytes(), xs = (long long)geo.xs_bytes(M), fixed = (long long)sizeof(DecSmem) + 1024;
+    const long long groups = (N + ch - 1) / ch;
+    int per_sm = groups > sms ? 2 : 1;
+    long long ring = 0;
+    for (; per_sm >= 1; --per_sm) {
+        ring = ((long long)dbulk::SM_SMEM / per_sm - fixed - xs) / stage;
+        if (ring >= 3 || per_sm == 1) break;
+    }
+    if (ring < 2) return d;
+    d.grid = (int)(groups < (long long)per_sm * sms ? groups : (long long)per_sm * sms);
+    const long long items = (groups + d.grid - 1) / d.grid * geo.nst;
+    ring = ring < DEC_RING ? ring : DEC_RING;
+    d.ring = (int)(ring < items ? ring : items);
+    d.smem = (size_t)(d.ring * stage + xs);
+    int j = 1;
+    while (j * 8 * DEC_CONSUMERS < geo.pitch - 16) j *= 2;
+    d.units = j * M <= 8 ? j : 0;
+    d.ok = true;
+    return d;
+}
+
+template <bool GLU, int NTG, int J, typename T>
+w4a8_status launch_decode(const DecPlan &d, DecArgs p, int ldp, cudaStream_t s) {
+    auto kern = k_mlp_decode<GLU, NTG, J, T>;
+    if (!raise_smem_limit(reinterpret_cast<const void *>(kern), DEC_DYN_SMEM)) return W4A8_ERR_CUDA;
+    const dbulk::Geometry geo(p.K);
+    CUtensorMap ta, tb;
+    auto map = [&](CUtensorMap *m, const uint8_t *W) {  // packed rows as 8-byte elements
+        return tc::make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, W, (uint64_t)(geo.kp / 8), (uint64_t)p.N,
+                               (uint64_t)ldp, (uint32_t)(geo.sb / 8), GLU ? 8 : 16, CU_TENSOR_MAP_SWIZZLE_NONE);
+    };
+    if (!map(&ta, p.a.Wp) || !map(&tb, p.b.Wp)) return W4A8_ERR_CUDA;
+    p.ring = d.ring;
+    return from_cuda(launch_pdl(kern, dim3(d.grid), dim3(DEC_THREADS), d.smem, s, ta, tb, p));
+}
+
+template <bool GLU, typename T>
+w4a8_status launch_decode_any(const DecPlan &d, const DecArgs &p, int ldp, cudaStream_t s) {
+    if (d.units == 1) return launch_decode<GLU, 1, 1, T>(d, p, ldp, s);
+    if (d.units == 2) return launch_decode<GLU, 1, 2, T>(d, p, ldp, s);
+    if (d.units == 4) return launch_decode<GLU, 1, 4, T>(d, p, ldp, s);
+    if (d.units == 8) return launch_decode<GLU, 1, 8, T>(d, p, ldp, s);
+    if (p.M <= 8) return launch_decode<GLU, 1, 0, T>(d, p, ldp, s);
+    return launch_decode<GLU, 2, 0, T>(d, p, ldp, s);
+}
+
+}  // namespace mlp
+}  // namespace w4a8
