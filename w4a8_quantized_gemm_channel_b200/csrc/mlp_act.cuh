@@ -43,6 +43,17 @@ __device__ __forceinline__ float act_value(float z) {
     return z;
 }
 
+// The activation by its code: for places that finish few values.
+__device__ __noinline__ float act_any(int act, float z) {
+    switch (act) {
+        case W4A8_ACT_RELU: return act_value<W4A8_ACT_RELU>(z);
+        case W4A8_ACT_SILU: return act_value<W4A8_ACT_SILU>(z);
+        case W4A8_ACT_GELU: return act_value<W4A8_ACT_GELU>(z);
+        case W4A8_ACT_GELU_TANH: return act_value<W4A8_ACT_GELU_TANH>(z);
+        default: return z;
+    }
+}
+
 // The activation and its derivative at z (ReLU's derivative at 0 is 0).
 template <int ACT>
 __device__ __forceinline__ void act_value_grad(float z, float &a, float &d) {
@@ -122,6 +133,20 @@ __device__ __forceinline__ float block_max(float a, float *red) {
 }
 
 // --------------------------------------------------------------- INT8 rows ---
+// The codes of eight consecutive values (scale s): word 0 = k0 k2 k4 k6, word
+// 1 = k1 k3 k5 k7. x s lies within 127 plus one rounding, so adding 1.5 2^23
+// rounds it to the nearest integer, ties to even, in the low bits (act_code8's
+// value; the clamp never binds) at two full-rate instructions a value, where
+// a conversion to integer runs at a quarter of the rate.
+__device__ __forceinline__ uint2 row_codes8(const float (&v)[8], float s) {
+    uint32_t q[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) q[b] = __float_as_uint(__fadd_rn(__fmul_rn(v[b], s), 12582912.0f));
+    const uint32_t e0 = __byte_perm(q[0], q[2], 0x0040), e1 = __byte_perm(q[4], q[6], 0x0040);
+    const uint32_t o0 = __byte_perm(q[1], q[3], 0x0040), o1 = __byte_perm(q[5], q[7], 0x0040);
+    return make_uint2(__byte_perm(e0, e1, 0x5410), __byte_perm(o0, o1, 0x5410));
+}
+
 // Step 3 of the layer on rows of T: the arithmetic of k_act_quant (the same
 // scales and codes for the same float32 values; a bfloat16 is widened
 // exactly), codes stored in the k-permuted order of the nibble unpack (k0 k2
@@ -160,26 +185,17 @@ k_quant_rows(const T *X, int M, int K, int ldx, int8_t *__restrict__ Xq, int ldq
         }
         const float s = act_scale_from_amax(block_max<THREADS>(amax, red));
         if (threadIdx.x == 0) sx[m] = s;
-        auto codes = [&](const float (&w)[8]) {
-            uint32_t even = 0, odd = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                even |= act_code8(w[2 * b], s, true) << (8 * b);
-                odd |= act_code8(w[2 * b + 1], s, true) << (8 * b);
-            }
-            return make_uint2(even, odd);
-        };
         if (in_regs) {
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
                 const int u = threadIdx.x + i * THREADS;
-                if (u < units) row[u] = codes(v[i]);
+                if (u < units) row[u] = row_codes8(v[i], s);
             }
         } else {
             for (int u = threadIdx.x; u < units; u += THREADS) {
                 float w[8];
                 ld_row8(x, 8 * u, K, vec != 0, w);
-                row[u] = codes(w);
+                row[u] = row_codes8(w, s);
             }
         }
     }

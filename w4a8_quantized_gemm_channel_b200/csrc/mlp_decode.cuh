@@ -27,7 +27,8 @@ namespace mlp {
 
 constexpr int DEC_TOK = 16;                 // rows at most
 constexpr int DEC_RING = 12;                // ring slots at most
-constexpr int DEC_THREADS = dbulk::THREADS; // 8 consumer warps and the producer
+constexpr int DEC_RED = 2;                  // groups whose warp sums may be waiting to be added
+constexpr int DEC_THREADS = dbulk::THREADS + 32;  // 8 consumer warps, the producer, the finishing warp
 constexpr int DEC_CONSUMERS = dbulk::CONSUMERS;
 
 struct DecArgs {
@@ -38,22 +39,40 @@ struct DecArgs {
     int M, K, N;
     Proj a, b;
     EpiArgs e;
-    int act, ring, early;
+    int act, ring, early, max_sb;
 };
 
+// Stages of a row's packed bytes: nst stages of sb bytes (a multiple of 64),
+// activation rows pitch bytes apart (all k of the stages + 16).
+struct DecGeo {
+    int kp, sb, nst, pitch;
+    __host__ __device__ DecGeo(int K, int max_sb) {
+        kp = packed_row_bytes(K);
+        const int kp64 = (kp + 63) / 64 * 64;
+        sb = kp64 < max_sb ? kp64 : max_sb;
+        nst = (kp + sb - 1) / sb;
+        pitch = 2 * sb * nst + 16;
+    }
+    __host__ __device__ int stage_bytes() const { return 16 * sb; }
+};
+
+template <int NTG>
 struct DecSmem {
     uint64_t full[DEC_RING], empty[DEC_RING];
+    uint64_t rfull[DEC_RED], rfree[DEC_RED];
     float part[dbulk::CONSUMER_WARPS];
-    float rsx[DEC_TOK];
-    int32_t red[dbulk::CONSUMER_WARPS][16][DEC_TOK + 1];
+    float rsx[8 * NTG];
+    int32_t red[DEC_RED][dbulk::CONSUMER_WARPS][16][8 * NTG + 1];
     int abort;
 };
-
-constexpr int DEC_DYN_SMEM = dbulk::SM_SMEM - (int)sizeof(DecSmem) - 1024;  // what a block may ask for
+// A block's static shared memory, up to where the dynamic part begins.
+template <int NTG>
+constexpr int dec_static() { return ((int)sizeof(DecSmem<NTG>) + 1023) / 1024 * 1024 + 1024; }
+constexpr int DEC_SM_SMEM = 226 * 1024;  // what blocks may take of an SM's shared memory
 
 // Quantize row r of X (J units of 8 values per thread) into xs.
 template <int J, typename T>
-__device__ __forceinline__ void dec_quantize(const DecArgs &p, int r, int ks, int8_t *xs, DecSmem &sm, int tid) {
+__device__ __forceinline__ void dec_quantize(const DecArgs &p, int r, int ks, int8_t *xs, float *part, float *rsx, int tid) {
     float v[J][8], a = 0.0f;
     const T *x = static_cast<const T *>(p.X) + (size_t)r * p.ldx;
 #pragma unroll
@@ -65,18 +84,18 @@ __device__ __forceinline__ void dec_quantize(const DecArgs &p, int r, int ks, in
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if ((tid & 31) == 0) sm.part[tid >> 5] = a;
+    if ((tid & 31) == 0) part[tid >> 5] = a;
     ptx::bar_sync(1, DEC_CONSUMERS);
-    a = sm.part[0];
+    a = part[0];
 #pragma unroll
-    for (int w = 1; w < dbulk::CONSUMER_WARPS; ++w) a = fmaxf(a, sm.part[w]);
+    for (int w = 1; w < dbulk::CONSUMER_WARPS; ++w) a = fmaxf(a, part[w]);
     ptx::bar_sync(1, DEC_CONSUMERS);  // part is rewritten by the next row
     const float s = act_scale_from_amax(a);
-    if (tid == 0) sm.rsx[r] = __frcp_rn(s);
+    if (tid == 0) rsx[r] = __frcp_rn(s);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int k = 8 * (tid + DEC_CONSUMERS * j);
-        if (k < ks) *reinterpret_cast<uint2 *>(xs + k) = dbulk::act_codes8_perm(v[j], s, k, p.K);
+        if (k < ks) *reinterpret_cast<uint2 *>(xs + k) = row_codes8(v[j], s);  // zeros past K
     }
 }
 
@@ -118,9 +137,9 @@ __global__ void __launch_bounds__(DEC_THREADS, 2)
 k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const DecArgs p) {
     constexpr int TOK = 8 * NTG;
     constexpr int CH = GLU ? 8 : 16;  // channels per group of 16 packed rows
-    __shared__ DecSmem sm;
+    __shared__ DecSmem<NTG> sm;
     extern __shared__ __align__(1024) uint8_t dyn_smem[];
-    const dbulk::Geometry geo(p.K);
+    const DecGeo geo(p.K, p.max_sb);
     const int sb = geo.sb, nst = geo.nst, pitch = geo.pitch, stage_bytes = geo.stage_bytes(), ks = pitch - 16;
     int8_t *xs = reinterpret_cast<int8_t *>(dyn_smem + (size_t)p.ring * stage_bytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -133,6 +152,10 @@ k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         for (int s = 0; s < p.ring; ++s) {
             ptx::mbar_init(&sm.full[s], 1);
             ptx::mbar_init(&sm.empty[s], dbulk::CONSUMER_WARPS);
+        }
+        for (int s = 0; s < DEC_RED; ++s) {
+            ptx::mbar_init(&sm.rfull[s], dbulk::CONSUMER_WARPS);
+            ptx::mbar_init(&sm.rfree[s], 1);
         }
         sm.abort = 0;
         ptx::fence_mbar_init();
@@ -172,11 +195,70 @@ k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
         return;
     }
 
+    if (warp == dbulk::CONSUMER_WARPS + 1) {
+        // -------------------------------------------------- finishing warp
+        // A group's sums over K meet in shared memory; the consumers only leave
+        // them there and go on, this warp adds them up and finishes the outputs
+        // (channel i % CH, row i / CH), its operands fetched a group ahead.
+        constexpr int OUTS = CH * TOK / 32;  // outputs per lane
+        const int ch = lane % CH;
+        griddep_wait();
+        float sa, ba, sc, bb, r[OUTS];
+        auto fetch = [&](int j) {
+            const int n = min(((int)blockIdx.x + j * (int)gridDim.x) * CH + ch, p.N - 1);
+            sa = ld_dep(p.a.sw + n);
+            ba = p.a.bias ? ld_dep(p.a.bias + n) : 0.0f;
+            sc = GLU ? ld_dep(p.b.sw + n) : 1.0f;
+            bb = GLU && p.b.bias ? ld_dep(p.b.bias + n) : 0.0f;
+            if (!GLU && p.e.R) {
+#pragma unroll
+                for (int o = 0; o < OUTS; ++o)
+                    r[o] = ld_elem(static_cast<const T *>(p.e.R) +
+                                   (size_t)min((32 * o + lane) / CH, p.M - 1) * p.e.ldr + n);
+            }
+        };
+        if (my_groups > 0) fetch(0);
+        for (int j = 0; j < my_groups; ++j) {
+            const int n = ((int)blockIdx.x + j * (int)gridDim.x) * CH + ch, rb = j % DEC_RED;
+            const float ra = __frcp_rn(sa) * 0.0625f, rc = __frcp_rn(sc) * 0.0625f;  // the sums hold 16 x the product
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.rfull[rb], (uint32_t)(j / DEC_RED) & 1u, abort))) return;
+            const float b0 = ba, b1 = bb;
+            float res[OUTS];
+#pragma unroll
+            for (int o = 0; o < OUTS; ++o) res[o] = r[o];
+            if (j + 1 < my_groups) fetch(j + 1);
+#pragma unroll
+            for (int o = 0; o < OUTS; ++o) {
+                const int tk = (32 * o + lane) / CH;
+                if (tk >= p.M || n >= p.N) continue;
+                int32_t ca = 0, cb = 0;
+#pragma unroll
+                for (int w = 0; w < dbulk::CONSUMER_WARPS; ++w) {
+                    ca += sm.red[rb][w][ch][tk];
+                    if constexpr (GLU) cb += sm.red[rb][w][8 + ch][tk];
+                }
+                const float rx = sm.rsx[tk];
+                const float z = dequant(ca, rx, ra, b0), u = GLU ? dequant(cb, rx, rc, b1) : 0.0f;
+                float y = act_any(p.act, z);
+                if constexpr (GLU) y *= u;
+                else if (p.e.R) y += res[o];
+                st_elem(static_cast<T *>(p.e.Y) + (size_t)tk * p.e.ldy + n, y);
+                if (p.e.Z) {
+                    st_elem(static_cast<T *>(p.e.Z) + (size_t)tk * p.e.ldz + n, z);
+                    if constexpr (GLU) st_elem(static_cast<T *>(p.e.U) + (size_t)tk * p.e.ldz + n, u);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sm.rfree[rb]);
+        }
+        return;
+    }
+
     // -------------------------------------------------------------- consumers
     const int g = lane >> 2, t = lane & 3;
     griddep_wait();
     if constexpr (J > 0) {
-        for (int r = 0; r < p.M; ++r) dec_quantize<J, T>(p, r, ks, xs + (size_t)r * pitch, sm, tid);
+        for (int r = 0; r < p.M; ++r) dec_quantize<J, T>(p, r, ks, xs + (size_t)r * pitch, sm.part, sm.rsx, tid);
     } else {
         const int per = ks / 16, have = min(p.ldq, ks) / 16;
 #pragma unroll 4
@@ -189,76 +271,29 @@ k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     }
     ptx::bar_sync(1, DEC_CONSUMERS);
 
-    // thread e < CH x TOK finishes channel e % CH of row e / CH
-    const int ch = tid % CH, tk = tid / CH;
-    const bool mine = tid < CH * TOK && tk < p.M;
-    const float rx = mine ? sm.rsx[tk] : 0.0f;
     for (int j = 0; j < my_groups; ++j) {
-        const int n = ((int)blockIdx.x + j * (int)gridDim.x) * CH + ch;
-        const bool ok = mine && n < p.N;
-        // needed after the group's MMAs: the loads overlap them
-        float sa = 1.0f, ba = 0.0f, sc = 1.0f, bb = 0.0f, r = 0.0f;
-        if (ok) {
-            sa = ld_dep(p.a.sw + n);
-            if (p.a.bias) ba = ld_dep(p.a.bias + n);
-            if constexpr (GLU) {
-                sc = ld_dep(p.b.sw + n);
-                if (p.b.bias) bb = ld_dep(p.b.bias + n);
-            } else {
-                if (p.e.R) r = ld_elem(static_cast<const T *>(p.e.R) + (size_t)tk * p.e.ldr + n);
-            }
-        }
         int32_t acc[NTG][2][4];
 #pragma unroll
         for (int i = 0; i < NTG; ++i)
 #pragma unroll
             for (int q = 0; q < 2; ++q) acc[i][q][0] = acc[i][q][1] = acc[i][q][2] = acc[i][q][3] = 0;
-        bool alive = true;
         for (int s = 0; s < nst; ++s) {
             const int it = j * nst + s, slot = it % p.ring;
-            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.full[slot], (uint32_t)(it / p.ring) & 1u, abort))) {
-                alive = false;
-                break;
-            }
+            if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.full[slot], (uint32_t)(it / p.ring) & 1u, abort))) return;
             dec_stage<NTG>(acc, dyn_smem + (size_t)slot * stage_bytes, sb, xs + 2 * sb * s, pitch, p.M, g, t, warp);
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&sm.empty[slot]);
         }
-        // the warps' C fragments (rows g, g + 8, columns 2t, 2t + 1) meet in shared memory
+        const int rb = j % DEC_RED;
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait(&sm.rfree[rb], ((uint32_t)(j / DEC_RED) & 1u) ^ 1u, abort))) return;
+        // C fragments: rows g, g + 8, columns 2t, 2t + 1
 #pragma unroll
         for (int i = 0; i < NTG; ++i)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-                sm.red[warp][g + 8 * (q >> 1)][8 * i + 2 * t + (q & 1)] = acc[i][0][q] + acc[i][1][q];
-        if (!ptx::bar_and(1, DEC_CONSUMERS, alive)) {
-            if (tid == 0) *abort = 1;  // lets the producer stop refilling
-            return;
-        }
-        if (ok) {
-            int32_t ca = 0, cb = 0;
-#pragma unroll
-            for (int w = 0; w < dbulk::CONSUMER_WARPS; ++w) {
-                ca += sm.red[w][ch][tk];
-                if constexpr (GLU) cb += sm.red[w][8 + ch][tk];
-            }
-            const float z = dequant(ca, rx, __frcp_rn(sa) * 0.0625f, ba);  // the sums hold 16 x the product
-            const float u = GLU ? dequant(cb, rx, __frcp_rn(sc) * 0.0625f, bb) : 0.0f;
-            float y = z;
-            switch (p.act) {
-                case W4A8_ACT_RELU: y = act_value<W4A8_ACT_RELU>(z); break;
-                case W4A8_ACT_SILU: y = act_value<W4A8_ACT_SILU>(z); break;
-                case W4A8_ACT_GELU: y = act_value<W4A8_ACT_GELU>(z); break;
-                case W4A8_ACT_GELU_TANH: y = act_value<W4A8_ACT_GELU_TANH>(z); break;
-                default: break;
-            }
-            y = GLU ? y * u : p.e.R ? y + r : y;
-            st_elem(static_cast<T *>(p.e.Y) + (size_t)tk * p.e.ldy + n, y);
-            if (p.e.Z) {
-                st_elem(static_cast<T *>(p.e.Z) + (size_t)tk * p.e.ldz + n, z);
-                if constexpr (GLU) st_elem(static_cast<T *>(p.e.U) + (size_t)tk * p.e.ldz + n, u);
-            }
-        }
-        ptx::bar_sync(1, DEC_CONSUMERS);  // red is rewritten by the next group
+                sm.red[rb][warp][g + 8 * (q >> 1)][8 * i + 2 * t + (q & 1)] = acc[i][0][q] + acc[i][1][q];
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.rfull[rb]);
     }
 }
 
@@ -267,44 +302,52 @@ k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 struct DecPlan {
     bool ok;
     int units;      // FUSED: units of 8 values per thread and row (1, 2, 4, 8), 0: INT8 rows
-    int grid, ring;
+    int grid, ring, max_sb;
     size_t smem;
 };
 
-// Two blocks per SM share its shared memory where the rows leave each a ring
-// of three stages, one block otherwise. FUSED while all rows are at most eight units of 8 values
-// per thread (2048 values a unit): beyond that every block's pass over X
-// costs more than the row pass's launch.
+// Blocks per SM (one or two) and stage size (rows of up to 2048 or 1024 packed
+// bytes): the pair that holds most bytes in flight beside the activation rows,
+// larger stages and two blocks first. FUSED while all rows are at most eight
+// units of 8 values per thread (2048 values a unit): beyond that every block's
+// pass over X costs more than the row pass's launch.
 inline DecPlan dec_plan(int M, int K, int N, int ch, int sms) {
     DecPlan d = {};
     if (M < 1 || M > DEC_TOK || K > dbulk::X16_MAX_K) return d;
-    const dbulk::Geometry geo(K);
-    const long long stage = geo.stage_bytes(), xs = (long long)geo.xs_bytes(M), fixed = (long long)sizeof(DecSmem) + 1024;
     const long long groups = (N + ch - 1) / ch;
-    int per_sm = groups > sms ? 2 : 1;
-    long long ring = 0;
-    for (; per_sm >= 1; --per_sm) {
-        ring = ((long long)dbulk::SM_SMEM / per_sm - fixed - xs) / stage;
-        if (ring >= 3 || per_sm == 1) break;
-    }
-    if (ring < 2) return d;
-    d.grid = (int)(groups < (long long)per_sm * sms ? groups : (long long)per_sm * sms);
-    const long long items = (groups + d.grid - 1) / d.grid * geo.nst;
-    ring = ring < DEC_RING ? ring : DEC_RING;
-    d.ring = (int)(ring < items ? ring : items);
-    d.smem = (size_t)(d.ring * stage + xs);
-    int j = 1;
-    while (j * 8 * DEC_CONSUMERS < geo.pitch - 16) j *= 2;
-    d.units = j * M <= 8 ? j : 0;
-    d.ok = true;
+    const long long fixed = (M <= 8 ? dec_static<1>() : dec_static<2>()) + 1024;
+    long long best = 0;
+    for (int max_sb = 2048; max_sb >= 1024; max_sb /= 2)
+        for (int per_sm = groups > sms ? 2 : 1; per_sm >= 1; --per_sm) {
+            const DecGeo geo(K, max_sb);
+            const long long xs = (long long)M * geo.pitch;
+            const long long grid = groups < (long long)per_sm * sms ? groups : (long long)per_sm * sms;
+            const long long items = (groups + grid - 1) / grid * geo.nst;
+            long long ring = (DEC_SM_SMEM / per_sm - fixed - xs) / geo.stage_bytes();
+            ring = ring < DEC_RING ? ring : DEC_RING;
+            ring = ring < items ? ring : items;
+            if (ring < 1 || (ring < 2 && items > 1)) continue;
+            const long long flight = per_sm * ring * geo.stage_bytes();
+            if (flight <= best) continue;
+            best = flight;
+            d.ok = true;
+            d.grid = (int)grid;
+            d.ring = (int)ring;
+            d.max_sb = max_sb;
+            d.smem = (size_t)(ring * geo.stage_bytes() + xs);
+            int j = 1;
+            while (j * 8 * DEC_CONSUMERS < geo.pitch - 16) j *= 2;
+            d.units = j * M <= 8 ? j : 0;
+        }
     return d;
 }
 
 template <bool GLU, int NTG, int J, typename T>
 w4a8_status launch_decode(const DecPlan &d, DecArgs p, int ldp, cudaStream_t s) {
     auto kern = k_mlp_decode<GLU, NTG, J, T>;
-    if (!raise_smem_limit(reinterpret_cast<const void *>(kern), DEC_DYN_SMEM)) return W4A8_ERR_CUDA;
-    const dbulk::Geometry geo(p.K);
+    constexpr int limit = 227 * 1024 - dec_static<NTG>();
+    if (!raise_smem_limit(reinterpret_cast<const void *>(kern), limit)) return W4A8_ERR_CUDA;
+    const DecGeo geo(p.K, d.max_sb);
     CUtensorMap ta, tb;
     auto map = [&](CUtensorMap *m, const uint8_t *W) {  // packed rows as 8-byte elements
         return tc::make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT64, W, (uint64_t)(geo.kp / 8), (uint64_t)p.N,
@@ -312,6 +355,7 @@ w4a8_status launch_decode(const DecPlan &d, DecArgs p, int ldp, cudaStream_t s) 
     };
     if (!map(&ta, p.a.Wp) || !map(&tb, p.b.Wp)) return W4A8_ERR_CUDA;
     p.ring = d.ring;
+    p.max_sb = d.max_sb;
     return from_cuda(launch_pdl(kern, dim3(d.grid), dim3(DEC_THREADS), d.smem, s, ta, tb, p));
 }
 
