@@ -306,9 +306,11 @@ struct DecPlan {
     size_t smem;
 };
 
-// Blocks per SM (one or two) and stage size (rows of up to 2048 or 1024 packed
-// bytes): the pair that holds most bytes in flight beside the activation rows,
-// larger stages and two blocks first. FUSED while all rows are at most eight
+// Two blocks per SM where their rings hold at least 48 KB each (one block's 8
+// warps alone do not keep up with the stream: 20.5 against 15.4 us at M = 8,
+// K = 4096, N = 11008, gated), one otherwise or where there are no more groups
+// than SMs. Stages of up to 2048 or 1024 packed bytes per row, whichever
+// leaves more bytes in flight beside the activation rows. FUSED while all rows are at most eight
 // units of 8 values per thread (2048 values a unit): beyond that every block's
 // pass over X costs more than the row pass's launch.
 inline DecPlan dec_plan(int M, int K, int N, int ch, int sms) {
@@ -316,20 +318,18 @@ inline DecPlan dec_plan(int M, int K, int N, int ch, int sms) {
     if (M < 1 || M > DEC_TOK || K > dbulk::X16_MAX_K) return d;
     const long long groups = (N + ch - 1) / ch;
     const long long fixed = (M <= 8 ? dec_static<1>() : dec_static<2>()) + 1024;
-    long long best = 0;
-    for (int max_sb = 2048; max_sb >= 1024; max_sb /= 2)
-        for (int per_sm = groups > sms ? 2 : 1; per_sm >= 1; --per_sm) {
+    for (int per_sm = groups > sms ? 2 : 1; per_sm >= 1 && !d.ok; --per_sm) {
+        long long best = per_sm == 2 ? 48 * 1024 - 1 : 0;
+        for (int max_sb = 2048; max_sb >= 1024; max_sb /= 2) {
             const DecGeo geo(K, max_sb);
             const long long xs = (long long)M * geo.pitch;
             const long long grid = groups < (long long)per_sm * sms ? groups : (long long)per_sm * sms;
             const long long items = (groups + grid - 1) / grid * geo.nst;
-            long long ring = (DEC_SM_SMEM / per_sm - fixed - xs) / geo.stage_bytes();
-            ring = ring < DEC_RING ? ring : DEC_RING;
+            const long long fit = (DEC_SM_SMEM / per_sm - fixed - xs) / geo.stage_bytes();
+            long long ring = fit < DEC_RING ? fit : DEC_RING;
             ring = ring < items ? ring : items;
-            if (ring < 1 || (ring < 2 && items > 1)) continue;
-            const long long flight = per_sm * ring * geo.stage_bytes();
-            if (flight <= best) continue;
-            best = flight;
+            if (fit < 2 || fit * geo.stage_bytes() <= best) continue;
+            best = fit * geo.stage_bytes();
             d.ok = true;
             d.grid = (int)grid;
             d.ring = (int)ring;
@@ -339,6 +339,7 @@ inline DecPlan dec_plan(int M, int K, int N, int ch, int sms) {
             while (j * 8 * DEC_CONSUMERS < geo.pitch - 16) j *= 2;
             d.units = j * M <= 8 ? j : 0;
         }
+    }
     return d;
 }
 
