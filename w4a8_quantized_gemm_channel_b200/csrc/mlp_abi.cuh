@@ -64,6 +64,15 @@ w4a8_status launch_quant_rows(const void *X, int M, int K, int ldx, const Worksp
     return from_cuda(e);
 }
 
+// Forward workspace: the INT8 rows and scales, then the partial tiles' slots.
+uint8_t *ws_parts(const Workspace &ws, int M) {
+    const uintptr_t end = reinterpret_cast<uintptr_t>(ws.sx) + sizeof(float) * (size_t)M;
+    return reinterpret_cast<uint8_t *>((end + 255) & ~uintptr_t(255));
+}
+size_t forward_workspace(int M, int K, int N, bool glu) {
+    return workspace_bytes_for(M, K, nullptr) + mlp::forward_plan(M, K, N, glu).part_bytes + 256;
+}
+
 // Few products: the CUDA-core form, whose launch is the cheapest.
 bool mlp_tiny(int M, int K, int N, int segs) { return (double)M * N * K * segs < 65536.0; }
 
@@ -97,12 +106,13 @@ w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a
     }
     if (path == W4A8_PATH_TC) {
         const int stages = (K + 255) / 256;
-        const mlp::PairArgs p = {M, N, K, stages, stages, ws.sx, a, b, ea, act, 0, 1};
-        const mlp::PairCall c = {a.Wp, b.Wp, N, ldp, ws.xq, M, ws.ldq, sms};
-        st = mlp::launch_pair_any<GLU ? mlp::FWD_GLU : mlp::FWD_LINEAR, T>(p, c, s);
+        const mlp::PairPlan plan = mlp::forward_plan(M, K, N, GLU);
+        const mlp::PairArgs p = {M, N, K, stages, stages, ws.sx, a, b, ea, act, 0, 1, nullptr};
+        const mlp::PairCall c = {a.Wp, b.Wp, N, ldp, ws.xq, M, ws.ldq};
+        st = mlp::launch_pair_any<GLU ? mlp::FWD_GLU : mlp::FWD_LINEAR, T>(plan, p, c, ws_parts(ws, M), s);
         if (st != W4A8_OK) return st;
         t_last_path = W4A8_PATH_TC;
-        t_last_launches = 2;
+        t_last_launches = plan.split ? 3 : 2;
         t_last_kernel = "k_mlp_pair";
         return W4A8_OK;
     }
@@ -139,24 +149,28 @@ struct GradWorkspace {
     int seg;     // columns of a segment: N rounded up to the product's k step
     int planes;
     size_t p_bytes, rs_bytes, part_bytes;
+    mlp::PairPlan plan;
     __half *P;
     float *rs, *part;
-    size_t total() const { return p_bytes + rs_bytes + part_bytes + 256; }
+    void *tiles;    // the product's partial tiles
+    size_t total() const { return p_bytes + rs_bytes + part_bytes + plan.part_bytes + 256; }
     void carve(void *base) {
         uintptr_t p = (reinterpret_cast<uintptr_t>(base) + 255) & ~uintptr_t(255);
         P = reinterpret_cast<__half *>(p);
         rs = reinterpret_cast<float *>(p + p_bytes);
         part = reinterpret_cast<float *>(p + p_bytes + rs_bytes);
+        tiles = reinterpret_cast<void *>(p + p_bytes + rs_bytes + part_bytes);
     }
 };
 
-GradWorkspace grad_layout(int M, int N, int segs, unsigned flags) {
+GradWorkspace grad_layout(int M, int K, int N, int segs, unsigned flags) {
     GradWorkspace g = {};
     g.seg = round_up(N, 128);
     g.planes = io_bf16(flags) ? 1 : 2;
     g.p_bytes = round256((size_t)g.planes * M * segs * g.seg * sizeof(__half));
     g.rs_bytes = round256((size_t)M * sizeof(float));
     g.part_bytes = round256((size_t)((M + mlp::BG_ROWS - 1) / mlp::BG_ROWS) * segs * N * sizeof(float));
+    g.plan = mlp::grad_plan(M, K, segs, g.seg, g.planes == 2);
     return g;
 }
 
@@ -191,14 +205,14 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
     if (st != W4A8_OK) return st;
     if (path == W4A8_PATH_TC) {
         const int seg_stages = ws.seg / (LO ? 64 : 128);
+        // (the row pass lets dependents start only once all earlier work is done: the weights are settled)
         const mlp::PairArgs p = {M, K, N, seg_stages, SEGS * seg_stages, ws.rs, {}, {},
-                                 {nullptr, dX, nullptr, nullptr, 0, lddx, 0}, 0, 0,
-                                 (flags & W4A8_STATIC_WEIGHTS) != 0};
-        const mlp::PairCall c = {Wa, Wb, N, ldp, ws.P, ws.planes * M, SEGS * ws.seg, device_info().sm_count};
-        st = mlp::launch_pair_any<LO ? mlp::BWD_TWO : mlp::BWD_ONE, T>(p, c, s);
+                                 {nullptr, dX, nullptr, nullptr, 0, lddx, 0}, 0, 0, 1, nullptr};
+        const mlp::PairCall c = {Wa, Wb, N, ldp, ws.P, ws.planes * M, SEGS * ws.seg};
+        st = mlp::launch_pair_any<LO ? mlp::BWD_TWO : mlp::BWD_ONE, T>(ws.plan, p, c, ws.tiles, s);
         if (st != W4A8_OK) return st;
         t_last_path = W4A8_PATH_TC;
-        t_last_launches = launches + 2;
+        t_last_launches = launches + (ws.plan.split ? 3 : 2);
         t_last_kernel = "k_mlp_pair";
         return W4A8_OK;
     }
@@ -228,7 +242,7 @@ w4a8_status mlp_grad_call(const void *dY, int M, int N, int lddy, const void *Z,
     if (!workspace || !aligned16(workspace)) return W4A8_ERR_WORKSPACE;
     if (workspace_bytes < w4a8_grad_workspace_size(M, K, N, GLU ? 2 : 1, flags)) return W4A8_ERR_WORKSPACE;
     if (!device_info().ok) return W4A8_ERR_UNSUPPORTED;
-    GradWorkspace ws = grad_layout(M, N, GLU ? 2 : 1, flags);
+    GradWorkspace ws = grad_layout(M, K, N, GLU ? 2 : 1, flags);
     ws.carve(workspace);
     auto run = [&](auto elem) {
         using T = decltype(elem);
@@ -247,12 +261,12 @@ extern "C" {
 size_t w4a8_act_workspace_size(int M, int K, int N, int projections, unsigned flags) {
     if (M < 0 || K < 1 || K > W4A8_ACT_MAX_K || N < 1 || projections < 1 || projections > 2) return 0;
     (void)flags;
-    return workspace_bytes_for(M, K, nullptr);
+    return forward_workspace(M, K, N, projections == 2);
 }
 
 size_t w4a8_grad_workspace_size(int M, int K, int N, int projections, unsigned flags) {
     if (M < 0 || K < 1 || K > W4A8_ACT_MAX_K || N < 1 || projections < 1 || projections > 2) return 0;
-    return grad_layout(M, N, projections, flags).total();
+    return grad_layout(M, K, N, projections, flags).total();
 }
 
 w4a8_status w4a8_linear_act(const void *X, int M, int K, int ldx, const uint8_t *Wp, int ldp, const float *sw, int N,

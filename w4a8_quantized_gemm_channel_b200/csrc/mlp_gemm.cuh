@@ -75,8 +75,14 @@ struct Shape {
     static constexpr int B_BYTES = 2 * B_TILE;
     // Slots per ring. 256 tokens leave shared memory for two widened stages.
     static constexpr int A_SLOTS = NT == 256 && SUBS == 2 ? 2 : 3;
-    static constexpr int P_SLOTS = NT == 256 ? 2 : 3;
+    static constexpr int P_SLOTS = NT == 256 ? 2 : NT == 128 ? 3 : 4;
     static constexpr int B_SLOTS = NT == 64 ? 4 : 3;
+    // Widening: both groups on every stage (half each), which has a stage
+    // ready soonest, or, where the MMAs of a stage are shorter than its
+    // widening, the groups on every second stage, which hides the latencies of
+    // one behind the other.
+    static constexpr bool TURNS = NT < 256;
+    static constexpr int WARPS_PER_STAGE = TURNS ? GROUP_WARPS : CONV_WARPS;
     static_assert(B_SLOTS >= A_SLOTS, "A-slot reuse waits on a token slot's barrier");
 };
 
@@ -88,10 +94,10 @@ struct alignas(1024) PairSmem {
     uint8_t packed[S::P_SLOTS][S::P_BYTES];
     uint8_t epi[EPI_SMEM];
     uint64_t pfull[S::P_SLOTS];   // packed weights landed
-    uint64_t pfree[S::P_SLOTS];   // packed weights read (8 widening warps)
+    uint64_t pfree[S::P_SLOTS];   // packed weights read (the stage's widening warps)
     uint64_t bfull[S::B_SLOTS];   // this CTA's tokens landed
     uint64_t empty[S::B_SLOTS];   // MMAs of the stage finished (both CTAs)
-    uint64_t ready[S::A_SLOTS];   // leader: both CTAs' operands there (16 warps)
+    uint64_t ready[S::A_SLOTS];   // leader: both CTAs' operands there (their widening warps)
     uint64_t acc_full[2];         // accumulator ready (both CTAs)
     uint64_t acc_empty[2];        // leader: both CTAs' epilogues drained (16 warps)
     uint64_t done;                // every MMA finished (both CTAs)
@@ -111,6 +117,43 @@ struct PairArgs {
     Proj a, b;
     EpiArgs e;          // gradient: Y = dX
     int act, tma_out, static_w;
+    uint32_t *parts;    // split calls: accumulators of partial tiles, else null
+};
+
+// The tiles' stages in one row, tile after tile, as the pairs share them out.
+// Whole tiles in turn; or, split, an equal run of stages per pair, whose first
+// and last tiles may be partial: their accumulators go to the pair's two
+// slots (2 pair: the run's first segment, 2 pair + 1: its last) and
+// k_mlp_join adds them up and finishes the tile.
+struct Run {
+    int tile, s0, s1;            // the current segment: stages [s0, s1) of a tile
+    long long at, end;           // split: position in the row, the run's end
+    int stages, num_tiles, step;
+    bool split, first;
+    __device__ __forceinline__ Run(const PairArgs &p, int num_tiles_, int pair, int npairs)
+        : stages(p.stages), num_tiles(num_tiles_), step(npairs), split(p.parts != nullptr), first(true) {
+        const long long all = (long long)num_tiles_ * p.stages;
+        at = split ? all * pair / npairs : (long long)pair * p.stages;
+        end = split ? all * (pair + 1) / npairs : all;
+        locate();
+    }
+    __device__ __forceinline__ void locate() {
+        tile = (int)(at / stages);
+        s0 = (int)(at - (long long)tile * stages);
+        s1 = split && end - at < stages - s0 ? s0 + (int)(end - at) : stages;
+    }
+    __device__ __forceinline__ bool valid() const { return at < end; }
+    __device__ __forceinline__ bool partial() const { return s1 - s0 != stages; }
+    __device__ __forceinline__ int slot(int pair) const { return 2 * pair + (first ? 0 : 1); }
+    __device__ __forceinline__ void next() {
+        at += split ? s1 - s0 : (long long)step * stages;
+        first = false;
+        if (valid()) locate();
+    }
+    // all stages of the run
+    __device__ __forceinline__ int total() const {
+        return split ? (int)(end - at) : (int)((end - at + (long long)step * stages - 1) / ((long long)step * stages)) * stages;
+    }
 };
 
 // ---- the MMA with both operands in shared memory ----
@@ -160,6 +203,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, abort));
 }
+// Untiled bulk store of this CTA's shared memory (16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(ptx::smem_addr(src)),
+                 "r"(bytes)
+                 : "memory");
+}
 __device__ __forceinline__ void bar_arrive(int id, int count) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
@@ -175,34 +224,40 @@ __device__ __forceinline__ void sts128(void *p, uint32_t a, uint32_t b, uint32_t
 // (16-byte chunk c of row s at chunk c ^ ((s >> 1) & 3)); widened sub-tiles
 // are 128-byte swizzled.
 //
-// Forward: group g takes sub-tile g, a thread one A row r. Nibbles stay in the
+// Forward: half g of a stage is sub-tile g, a thread has one A row r of it. Nibbles stay in the
 // high half of their byte (16 q), in the order the INT8 rows are stored in.
 // Gated: A rows 32 w + 0..15 are gate channels 16 w + .., 32 w + 16..31 the
 // same up channels (the packed tile holds 64 gate rows, then 64 up rows).
 //
 // Gradient: a thread takes chunks c of packed row n (one n, 128 k): c = tid / 64
-// and that + 2 of sub-tile g, or with two planes (one sub-tile) c = 2 g + tid / 64.
+// and that + 2 of sub-tile g (half g), or with two planes (one sub-tile) c = 2 g + tid / 64.
 // Nibble u of q + 8 is put under the FP16 exponent of 1024 (1024 + u, exact)
 // and 1032 is subtracted. Masking words of eight codes gives them in the order
 // k0 k4 k1 k5 k2 k6 k3 k7, undone by the epilogue's row index.
 template <int MODE>
 constexpr int pieces() { return MODE == BWD_TWO ? 1 : MODE == BWD_ONE ? 2 : 4; }
 
-template <int MODE>
-__device__ __forceinline__ void load_pieces(uint4 (&v)[pieces<MODE>()], const uint8_t *packed, int g, int tid) {
-    if constexpr (MODE == FWD_LINEAR || MODE == FWD_GLU) {
-        const int r = tid, s = MODE == FWD_GLU ? ((r & 16) << 2) + ((r >> 5) << 4) + (r & 15) : r;
-        const uint8_t *row = packed + g * (128 * 64) + s * 64;
+// WHOLE: the group takes the whole stage, its other half's pieces after its own.
+template <int MODE, bool WHOLE>
+__device__ __forceinline__ void load_pieces(uint4 (&v)[pieces<MODE>() * (WHOLE ? 2 : 1)], const uint8_t *packed, int g,
+                                            int tid) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = ptx::lds128(row + 16 * (c ^ ((s >> 1) & 3)));
-    } else {
-        const int n = tid & 63, c = tid >> 6;
-        const uint8_t *row = packed + (MODE == BWD_ONE ? g * (64 * 64) : 0) + n * 64;
-        if constexpr (MODE == BWD_ONE) {
-            v[0] = ptx::lds128(row + 16 * (c ^ ((n >> 1) & 3)));
-            v[1] = ptx::lds128(row + 16 * ((c + 2) ^ ((n >> 1) & 3)));
+    for (int h = 0; h < (WHOLE ? 2 : 1); ++h) {
+        const int half = WHOLE ? h : g;
+        if constexpr (MODE == FWD_LINEAR || MODE == FWD_GLU) {
+            const int r = tid, s = MODE == FWD_GLU ? ((r & 16) << 2) + ((r >> 5) << 4) + (r & 15) : r;
+            const uint8_t *row = packed + half * (128 * 64) + s * 64;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[4 * h + c] = ptx::lds128(row + 16 * (c ^ ((s >> 1) & 3)));
         } else {
-            v[0] = ptx::lds128(row + 16 * ((2 * g + c) ^ ((n >> 1) & 3)));
+            const int n = tid & 63, c = tid >> 6;
+            const uint8_t *row = packed + (MODE == BWD_ONE ? half * (64 * 64) : 0) + n * 64;
+            if constexpr (MODE == BWD_ONE) {
+                v[2 * h] = ptx::lds128(row + 16 * (c ^ ((n >> 1) & 3)));
+                v[2 * h + 1] = ptx::lds128(row + 16 * ((c + 2) ^ ((n >> 1) & 3)));
+            } else {
+                v[h] = ptx::lds128(row + 16 * ((2 * half + c) ^ ((n >> 1) & 3)));
+            }
         }
     }
 }
@@ -224,22 +279,28 @@ __device__ __forceinline__ void widen_chunk(const uint4 &v, uint8_t *slot, int n
     }
 }
 
-template <int MODE>
-__device__ __forceinline__ void widen_pieces(const uint4 (&v)[pieces<MODE>()], uint8_t *slot, int g, int tid) {
-    if constexpr (MODE == FWD_LINEAR || MODE == FWD_GLU) {
-        const int r = tid;
-        uint8_t *row = slot + g * SUB_BYTES + r * 128;
-        constexpr uint32_t H = 0xF0F0F0F0u;
+template <int MODE, bool WHOLE>
+__device__ __forceinline__ void widen_pieces(const uint4 (&v)[pieces<MODE>() * (WHOLE ? 2 : 1)], uint8_t *slot, int g,
+                                             int tid) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            sts128(row + 16 * ((2 * c) ^ (r & 7)), (v[c].x << 4) & H, v[c].x & H, (v[c].y << 4) & H, v[c].y & H);
-            sts128(row + 16 * ((2 * c + 1) ^ (r & 7)), (v[c].z << 4) & H, v[c].z & H, (v[c].w << 4) & H, v[c].w & H);
+    for (int h = 0; h < (WHOLE ? 2 : 1); ++h) {
+        const int half = WHOLE ? h : g;
+        if constexpr (MODE == FWD_LINEAR || MODE == FWD_GLU) {
+            const int r = tid;
+            uint8_t *row = slot + half * SUB_BYTES + r * 128;
+            constexpr uint32_t H = 0xF0F0F0F0u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 &w = v[4 * h + c];
+                sts128(row + 16 * ((2 * c) ^ (r & 7)), (w.x << 4) & H, w.x & H, (w.y << 4) & H, w.y & H);
+                sts128(row + 16 * ((2 * c + 1) ^ (r & 7)), (w.z << 4) & H, w.z & H, (w.w << 4) & H, w.w & H);
+            }
+        } else if constexpr (MODE == BWD_ONE) {
+            widen_chunk(v[2 * h], slot + half * SUB_BYTES, tid & 63, tid >> 6);
+            widen_chunk(v[2 * h + 1], slot + half * SUB_BYTES, tid & 63, (tid >> 6) + 2);
+        } else {
+            widen_chunk(v[h], slot, tid & 63, 2 * half + (tid >> 6));
         }
-    } else if constexpr (MODE == BWD_ONE) {
-        widen_chunk(v[0], slot + g * SUB_BYTES, tid & 63, tid >> 6);
-        widen_chunk(v[1], slot + g * SUB_BYTES, tid & 63, (tid >> 6) + 2);
-    } else {
-        widen_chunk(v[0], slot, tid & 63, 2 * g + (tid >> 6));
     }
 }
 
@@ -333,7 +394,10 @@ __device__ __forceinline__ void copy_out(const uint8_t *stg, void *out, int ld, 
     }
 }
 
-// Staging of a call: each group owns half of EPI_SMEM, one or two sets of tiles.
+// Staging of a call: each group owns half of EPI_SMEM, as one set of tiles or
+// two sets of half that size. A partial tile's unit (raw accumulators, all 128
+// lanes) takes 8 KB of a set.
+constexpr int RAW_UNIT = UNIT * ROWS_CTA * 4;
 template <int MODE, typename T>
 struct Staging {
     static constexpr int COLS = MODE == FWD_GLU ? 64 : 128;
@@ -341,14 +405,21 @@ struct Staging {
     int outs, sets;
     __device__ __forceinline__ explicit Staging(const EpiArgs &e) {
         outs = 1 + ((MODE == FWD_LINEAR || MODE == FWD_GLU) && e.Z ? (MODE == FWD_GLU ? 2 : 1) : 0);
-        sets = 2 * outs * TILE * EPI_GROUPS <= EPI_SMEM ? 2 : 1;
+        sets = outs * TILE <= EPI_SMEM / EPI_GROUPS / 2 ? 2 : 1;
     }
     __device__ __forceinline__ uint8_t *at(uint8_t *epi, int group, int set) const {
-        return epi + group * (EPI_SMEM / EPI_GROUPS) + set * outs * TILE;
+        return epi + group * (EPI_SMEM / EPI_GROUPS) + set * (EPI_SMEM / EPI_GROUPS / 2);
     }
 };
 static_assert(Staging<FWD_LINEAR, float>::TILE * 2 * EPI_GROUPS <= EPI_SMEM &&
-              Staging<FWD_GLU, float>::TILE * 3 * EPI_GROUPS <= EPI_SMEM, "one set of every call fits");
+              Staging<FWD_GLU, float>::TILE * 3 * EPI_GROUPS <= EPI_SMEM &&
+              RAW_UNIT * 2 * EPI_GROUPS <= EPI_SMEM, "one set of every call fits, and two of raw units");
+
+// Where a partial tile's unit goes: slot, CTA of the pair, unit; rows of 128 lanes.
+template <int NT>
+__host__ __device__ inline size_t part_offset(int slot, int rank, int unit) {
+    return (((size_t)slot * 2 + rank) * (NT / UNIT) + unit) * (UNIT * ROWS_CTA);
+}
 
 template <int MODE, int NT, typename T>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
@@ -368,20 +439,20 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
     const int pair = (int)blockIdx.x >> 1, npairs = (int)gridDim.x >> 1;
     const int tiles_m = (p.M + NT - 1) / NT, tiles_n = (p.N + TILE_ROWS - 1) / TILE_ROWS;
     const int num_tiles = tiles_m * tiles_n;
-    const int my_tiles = (num_tiles - pair + npairs - 1) / npairs;
-    const int total = my_tiles * p.stages;
+    const Run run0(p, num_tiles, pair, npairs);
+    const int total = run0.valid() ? run0.total() : 0;
     volatile int *abort = &sm.abort;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S::P_SLOTS; ++s) {
             ptx::mbar_init(&sm.pfull[s], 1);
-            ptx::mbar_init(&sm.pfree[s], CONV_WARPS);
+            ptx::mbar_init(&sm.pfree[s], S::WARPS_PER_STAGE);
         }
         for (int s = 0; s < B_SLOTS; ++s) {
             ptx::mbar_init(&sm.bfull[s], 1);
             ptx::mbar_init(&sm.empty[s], 1);
         }
-        for (int a = 0; a < A_SLOTS; ++a) ptx::mbar_init(&sm.ready[a], 2 * CONV_WARPS);
+        for (int a = 0; a < A_SLOTS; ++a) ptx::mbar_init(&sm.ready[a], 2 * S::WARPS_PER_STAGE);
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&sm.acc_full[b], 1);
             ptx::mbar_init(&sm.acc_empty[b], 2 * 4 * EPI_GROUPS);
@@ -427,9 +498,16 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
     // Static weights: the first stages' packed tiles are requested before the
     // dependency wait; the tokens are read only after it.
     const int pre_w = p.static_w ? min(S::P_SLOTS, total) : 0;
-    if (warp == 0 && lane == 0)
-        for (int it = 0; it < pre_w; ++it)
-            load_weights(it, (pair + (it / p.stages) * npairs) / tiles_m, it % p.stages);
+    if (warp == 0 && lane == 0) {
+        Run r = run0;
+        for (int it = 0, st = r.s0; it < pre_w; ++it) {
+            load_weights(it, r.tile / tiles_m, st);
+            if (++st == r.s1) {
+                r.next();
+                st = r.s0;
+            }
+        }
+    }
     __syncwarp();
     griddep_launch_dependents();
     griddep_wait();
@@ -446,10 +524,10 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             uint32_t phase = 0, issued = (1u << pre_w) - 1u, last_par = 0;
             if (!w) issued = 0;
             bool ok = true;
-            for (int tile = pair; tile < num_tiles && ok; tile += npairs) {
-                const int n_tile = tile / tiles_m;
-                const int m0 = (tile % tiles_m) * NT + rank * HT;
-                for (int st = 0; st < p.stages; ++st, ++it) {
+            for (Run r = run0; r.valid() && ok; r.next()) {
+                const int n_tile = r.tile / tiles_m;
+                const int m0 = (r.tile % tiles_m) * NT + rank * HT;
+                for (int st = r.s0; st < r.s1; ++st, ++it) {
                     if (!w || it >= pre_w) {
                         if (!ptx::mbar_wait(&freed[slot], phase ^ 1, abort)) { ok = false; break; }
                         if (w) {
@@ -488,37 +566,39 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                                     : sdesc_mn_sw128(ptx::smem_addr(sm.a[0]), 64 * 128);
             const uint64_t b0 = ptx::sdesc_k_sw128(ptx::smem_addr(sm.b[0]));
             constexpr uint32_t A_STEP = FWD ? 32 : 2048;  // bytes per MMA along the contraction
-            int slot = 0, as = 0, st = 0, buf = 0, left = p.depth;
-            int seg_st = 0;
+            int slot = 0, as = 0, buf = 0;
             uint32_t aphase = 0, bphase = 0;
-            for (int it = 0; it < total; ++it) {
-                if (st == 0 && !warp_wait(&sm.acc_empty[buf], bphase ^ 1u, abort)) break;
-                if (!warp_wait(&sm.ready[as], aphase, abort)) break;
-                ptx::tc_fence_after();
+            bool ok = true;
+            for (Run r = run0; r.valid() && ok; r.next()) {
+                if (!warp_wait(&sm.acc_empty[buf], bphase ^ 1u, abort)) break;
                 const uint32_t d = tmem + (uint32_t)(buf * 256);
-                const uint64_t a = a0 + (uint32_t)(as * S::A_BYTES / 16), b = b0 + (uint32_t)(slot * S::B_BYTES / 16);
-                auto mma = [&](int i) {
-                    const int sub = S::SUBS == 2 ? i >> 2 : 0, kk = i & 3;
-                    const uint64_t ad = a + (uint32_t)((sub * SUB_BYTES + kk * A_STEP) / 16);
-                    const uint64_t bd = b + (uint32_t)(((i >> 2) * S::B_TILE + 32 * kk) / 16);
-                    if (one) mma_ss2<FWD>(d, ad, bd, idesc, (st | i) != 0);
-                };
+                int seg_st = r.s0 >= p.seg_stages ? r.s0 - p.seg_stages : r.s0;
+                int left = p.depth - S::STEP * seg_st;
+                for (int st = r.s0; st < r.s1; ++st) {
+                    ok = warp_wait(&sm.ready[as], aphase, abort);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint64_t a = a0 + (uint32_t)(as * S::A_BYTES / 16), b = b0 + (uint32_t)(slot * S::B_BYTES / 16);
+                    auto mma = [&](int i) {
+                        const int sub = S::SUBS == 2 ? i >> 2 : 0, kk = i & 3;
+                        const uint64_t ad = a + (uint32_t)((sub * SUB_BYTES + kk * A_STEP) / 16);
+                        const uint64_t bd = b + (uint32_t)(((i >> 2) * S::B_TILE + 32 * kk) / 16);
+                        if (one) mma_ss2<FWD>(d, ad, bd, idesc, st != r.s0 || i != 0);
+                    };
 #pragma unroll
-                for (int i = 0; i < 4; ++i) mma(i);
-                if (S::SUBS == 1 || left > S::SUB) {  // else the second sub-tile lies past the contraction's end
+                    for (int i = 0; i < 4; ++i) mma(i);
+                    if (S::SUBS == 1 || left > S::SUB) {  // else the second sub-tile lies past the contraction's end
 #pragma unroll
-                    for (int i = 4; i < 8; ++i) mma(i);
+                        for (int i = 4; i < 8; ++i) mma(i);
+                    }
+                    if (one) tcp::mma_commit2_both(&sm.empty[slot]);
+                    left -= S::STEP;
+                    if (++seg_st == p.seg_stages) { seg_st = 0; left = p.depth; }
+                    if (++slot == B_SLOTS) slot = 0;
+                    if (++as == A_SLOTS) { as = 0; aphase ^= 1u; }
                 }
-                if (one) tcp::mma_commit2_both(&sm.empty[slot]);
-                left -= S::STEP;
-                if (++seg_st == p.seg_stages) { seg_st = 0; left = p.depth; }
-                if (++st == p.stages) {
-                    if (one) tcp::mma_commit2_both(&sm.acc_full[buf]);
-                    st = 0;
-                    if (++buf == 2) { buf = 0; bphase ^= 1u; }
-                }
-                if (++slot == B_SLOTS) slot = 0;
-                if (++as == A_SLOTS) { as = 0; aphase ^= 1u; }
+                if (ok && one) tcp::mma_commit2_both(&sm.acc_full[buf]);
+                if (++buf == 2) { buf = 0; bphase ^= 1u; }
             }
             if (total > 0 && one) tcp::mma_commit2_both(&sm.done);
         }
@@ -526,29 +606,41 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         // ---------------------------------------------------- widening (each CTA: its 128 rows)
         const int grp = (warp - FIRST_CONV) / GROUP_WARPS;
         const int tid = (threadIdx.x - 32 * FIRST_CONV) % (32 * GROUP_WARPS);
-        int ps = 0, bs = 0, as = 0;
-        int old = B_SLOTS - A_SLOTS;    // the token slot of iteration it - A_SLOTS
-        uint32_t pphase = 0, bphase = 0, ophase = 1;  // it starts below 0: its phase flips as it wraps
-        for (int it = 0; it < total; ++it) {
-            // The packed bytes come into registers, and their slot is free
-            // again, before the wait for the A slot: what follows the MMAs'
-            // end is only the widening and its stores.
+        constexpr int STRIDE = S::TURNS ? CONV_GROUPS : 1;   // stages from one of this group's to its next
+        constexpr int PIECES = pieces<MODE>() * (S::TURNS ? 2 : 1);
+        const int it0 = S::TURNS ? grp : 0;
+        int ps = it0, bs = it0, as = it0 % A_SLOTS;
+        int old = (it0 + B_SLOTS - A_SLOTS) % B_SLOTS;        // the token slot of iteration it - A_SLOTS
+        uint32_t pphase = 0, bphase = 0;
+        uint32_t ophase = it0 >= A_SLOTS ? 0 : 1;             // below 0 it has the parity before the first
+        for (int it = it0; it < total; it += STRIDE) {
+            // The packed bytes come into registers before the wait for the A
+            // slot: what follows the MMAs' end is only the widening and its
+            // stores. (Their slot is given back after the stores, which need
+            // the values: given back right behind the loads it was refilled
+            // under them.)
+            // (A group that takes every second stage waits for the A slot first:
+            // the stage whose MMAs it then knows done had the same packed slot,
+            // so the parity of its own wait cannot be mistaken for the phase
+            // before, which the other group consumes.)
+            if (S::TURNS && it >= A_SLOTS && !warp_wait(&sm.empty[old], ophase, abort)) break;
             if (!warp_wait(&sm.pfull[ps], pphase, abort)) break;
-            uint4 v[pieces<MODE>()];
-            load_pieces<MODE>(v, sm.packed[ps], grp, tid);
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&sm.pfree[ps]);
+            uint4 v[PIECES];
+            load_pieces<MODE, S::TURNS>(v, sm.packed[ps], grp, tid);
             if (!warp_wait(&sm.bfull[bs], bphase, abort)) break;
             // the A slot was last read by the MMAs of iteration it - A_SLOTS
-            if (it >= A_SLOTS && !warp_wait(&sm.empty[old], ophase, abort)) break;
-            widen_pieces<MODE>(v, sm.a[as], grp, tid);
+            if (!S::TURNS && it >= A_SLOTS && !warp_wait(&sm.empty[old], ophase, abort)) break;
+            widen_pieces<MODE, S::TURNS>(v, sm.a[as], grp, tid);
             tcp::fence_proxy_async_smem();  // the slot's generic writes, before the MMA reads them
             __syncwarp();
-            if (lane == 0) tcp::mbar_arrive_leader(&sm.ready[as]);
-            if (++ps == S::P_SLOTS) { ps = 0; pphase ^= 1u; }
-            if (++bs == B_SLOTS) { bs = 0; bphase ^= 1u; }
-            if (++old == B_SLOTS) { old = 0; ophase ^= 1u; }
-            if (++as == A_SLOTS) as = 0;
+            if (lane == 0) {
+                ptx::mbar_arrive(&sm.pfree[ps]);
+                tcp::mbar_arrive_leader(&sm.ready[as]);
+            }
+            if ((ps += STRIDE) >= S::P_SLOTS) { ps -= S::P_SLOTS; pphase ^= 1u; }
+            if ((bs += STRIDE) >= B_SLOTS) { bs -= B_SLOTS; bphase ^= 1u; }
+            if ((old += STRIDE) >= B_SLOTS) { old -= B_SLOTS; ophase ^= 1u; }
+            if ((as += STRIDE) >= A_SLOTS) as -= A_SLOTS;
         }
     } else if (warp >= FIRST_EPI) {
         // ---------------------------------------------------- epilogue (each CTA: its 128 TMEM lanes)
@@ -566,10 +658,10 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         const bool res = FWD && !GLU && p.e.R != nullptr;
         int buf = 0, set = 0;
         uint32_t acc_phase = 0;
-        for (int tile = pair; tile < num_tiles; tile += npairs) {
-            const int n_tile = tile / tiles_m, m_base = (tile % tiles_m) * NT;
+        for (Run run = run0; run.valid(); run.next()) {
+            const int n_tile = run.tile / tiles_m, m_base = (run.tile % tiles_m) * NT;
             const int n_base = n_tile * TILE_ROWS + rank * COLS, n = n_base + col;
-            const bool n_ok = n < p.N;
+            const bool n_ok = n < p.N, partial = run.partial();
             if (ea < NT) {
                 const float t = m_base + ea < p.M ? ld_dep(p.tok + m_base + ea) : 1.0f;
                 sm.tok[ea] = FWD ? __frcp_rn(t) : t;
@@ -583,10 +675,8 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             }
             // One decision for all warps (this barrier also publishes the table).
             if (!ptx::bar_and(BAR_EPI, 128 * EPI_GROUPS, ptx::mbar_wait(&sm.acc_full[buf], acc_phase, abort))) {
-                if (p.tma_out) {  // let the store warp leave too
-                    sm.stop = 1;
-                    bar_arrive(BAR_STAGED + 2 * eg + set, 160);
-                }
+                sm.stop = 1;  // let the store warp leave too
+                bar_arrive(BAR_STAGED + 2 * eg + set, 160);
                 break;
             }
             ptx::tc_fence_after();
@@ -594,15 +684,13 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             for (int c0 = UNIT * eg; c0 < NT; c0 += UNIT * EPI_GROUPS) {
                 const int m0 = m_base + c0;
                 if (m0 >= p.M) break;
-                // the staging tiles are free: the store warp has seen their last
-                // stores read, or the group itself has copied them out
-                if (p.tma_out) ptx::bar_sync(BAR_FREE + 2 * eg + set, 160);
-                else ptx::bar_sync(BAR_GROUP + eg, 128);
+                // the set is free: the store warp has seen its last stores read
+                ptx::bar_sync(BAR_FREE + 2 * eg + set, 160);
                 uint8_t *stg = sg.at(sm.epi, eg, set);
                 const uint32_t st = ptx::smem_addr(stg) + (uint32_t)(col * (int)sizeof(T));
                 uint32_t v[16];
                 float r[16];
-                if (res) {  // indexes past the edges repeat the last row or column
+                if (res && !partial) {  // indexes past the edges repeat the last row or column
                     const T *R = static_cast<const T *>(p.e.R) + min(n, p.N - 1);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) r[j] = ld_elem(R + (size_t)min(m0 + j, p.M - 1) * p.e.ldr);
@@ -610,7 +698,12 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                 ptx::tmem_ld_32x32b_x16(tmem + lane_base + (uint32_t)(buf * 256 + c0), v);
                 ptx::tmem_wait_ld();
                 const float *tok = sm.tok + c0;
-                if constexpr (FWD) {
+                if (partial) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ptx::smem_addr(stg) + (uint32_t)(j * ROWS_CTA + et) * 4),
+                                     "r"(v[j]));
+                } else if constexpr (FWD) {
 #define W4A8_UNIT(A) fwd_unit_any<A, GLU, T>(p.e.Z != nullptr, res, v, r, tok, rsw, b, lane, st, TILE)
                     switch (p.act) {
                         case W4A8_ACT_NONE: W4A8_UNIT(W4A8_ACT_NONE); break;
@@ -627,15 +720,15 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                     for (int j = 0; j < 16; ++j) y[j] *= __uint_as_float(v[j]);
                     sts_column(st, COLS * (int)sizeof(T), y, T());
                 }
-                if (p.tma_out) {
+                if (p.tma_out || partial) {
                     tcp::fence_proxy_async_smem();  // the staging writes, before the store reads them
-                    bar_arrive(BAR_STAGED + 2 * eg + set, 160);
                 } else {
                     ptx::bar_sync(BAR_GROUP + eg, 128);
                     copy_out<COLS, T>(stg, p.e.Y, p.e.ldy, m0, p.M, n_base, p.N, et);
                     if (sg.outs > 1) copy_out<COLS, T>(stg + TILE, p.e.Z, p.e.ldz, m0, p.M, n_base, p.N, et);
                     if (sg.outs > 2) copy_out<COLS, T>(stg + 2 * TILE, p.e.U, p.e.ldz, m0, p.M, n_base, p.N, et);
                 }
+                bar_arrive(BAR_STAGED + 2 * eg + set, 160);
                 if (sg.sets == 2) set ^= 1;
             }
             ptx::tc_fence_before();
@@ -644,18 +737,19 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             if (++buf == 2) { buf = 0; acc_phase ^= 1; }
             ptx::bar_sync(BAR_EPI, 128 * EPI_GROUPS);  // the table is rewritten next tile
         }
-    } else if (warp == 3 && p.tma_out) {
+    } else if (warp == 3) {
         // ---------------------------------------------------- output stores
         // Its own warp, so that neither the store's issue nor the wait for the
         // staging tiles to be read holds the epilogue up. Units in order: the
-        // groups in turn, each group's sets in turn.
+        // groups in turn, each group's sets in turn. (Units that the epilogue
+        // has copied out itself only pass through.)
         const Staging<MODE, T> sg(p.e);
         constexpr int COLS = sg.COLS, TILE = sg.TILE;
         int unit[EPI_GROUPS] = {};  // units each group has had
         for (int i = 0; i < EPI_GROUPS * sg.sets; ++i) bar_arrive(BAR_FREE + 2 * (i % EPI_GROUPS) + i / EPI_GROUPS, 160);
         bool stop = false;
-        for (int tile = pair; tile < num_tiles && !stop; tile += npairs) {
-            const int n_base = (tile / tiles_m) * TILE_ROWS + rank * COLS, m_base = (tile % tiles_m) * NT;
+        for (Run run = run0; run.valid() && !stop; run.next()) {
+            const int n_base = (run.tile / tiles_m) * TILE_ROWS + rank * COLS, m_base = (run.tile % tiles_m) * NT;
             const int units = (min(NT, p.M - m_base) + UNIT - 1) / UNIT;
             for (int i = 0; i < units; ++i) {
                 const int eg = i % EPI_GROUPS, m0 = m_base + i * UNIT;
@@ -665,7 +759,9 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                 if (stop) break;
                 if (lane == 0) {
                     const uint8_t *stg = sg.at(sm.epi, eg, set);
-                    if (n_base < p.N) {
+                    if (run.partial()) {
+                        bulk_s2g(p.parts + part_offset<NT>(run.slot(pair), rank, i), stg, RAW_UNIT);
+                    } else if (p.tma_out && n_base < p.N) {
                         tcp::tma_store_2d(&tm_y, stg, n_base, m0);
                         if (sg.outs > 1) tcp::tma_store_2d(&tm_z, stg + TILE, n_base, m0);
                         if (sg.outs > 2) tcp::tma_store_2d(&tm_u, stg + 2 * TILE, n_base, m0);
@@ -703,7 +799,125 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
     }
 }
 
+// Finishes the tiles that k_mlp_pair left in parts. Block (b, unit): the tile
+// that holds the boundary between the runs of pairs b and b + 1, if b is the
+// first boundary inside it; one unit of 16 tokens; thread: a TMEM lane of one
+// of the pair's CTAs. Parts are added in the order of their stages, so results
+// repeat bit for bit (INT32 sums are exact anyway).
+template <int MODE, int NT, typename T>
+__global__ void __launch_bounds__(256)
+k_mlp_join(const PairArgs p, int npairs) {
+    constexpr bool FWD = Shape<MODE, NT>::FWD, GLU = MODE == FWD_GLU;
+    constexpr int COLS = GLU ? 64 : 128, TILE_ROWS = 2 * COLS;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int tiles_m = (p.M + NT - 1) / NT, tiles_n = (p.N + TILE_ROWS - 1) / TILE_ROWS;
+    const long long all = (long long)tiles_m * tiles_n * p.stages;
+    auto bound = [&](int i) { return all * i / npairs; };  // where pair i's run begins
+    const int b = blockIdx.x, unit = blockIdx.y;
+    const long long x = bound(b + 1);
+    const int tile = (int)(x / p.stages);
+    const long long t0 = (long long)tile * p.stages, t1 = t0 + p.stages;
+    if (x == t0 || x >= all || bound(b) > t0) return;  // no tile inside, or an earlier boundary's
+    const int m0 = (tile % tiles_m) * NT + unit * UNIT;
+    if (m0 >= p.M) return;
+    const int rank = threadIdx.x >> 7, et = threadIdx.x & 127, lane = et & 31;
+    uint32_t v[16];
+    for (int q = b; q < npairs && bound(q) < t1; ++q) {
+        if (bound(q + 1) == bound(q)) continue;
+        // the tile is the first of q's run unless the run began in another tile
+        const int slot = 2 * q + (q == b && bound(q) < t0 ? 1 : 0);
+        const uint32_t *src = p.parts + part_offset<NT>(slot, rank, unit) + et;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            uint32_t w;
+            asm volatile("ld.global.u32 %0, [%1];" : "=r"(w) : "l"(src + j * ROWS_CTA));
+            if (q == b) v[j] = w;
+            else if constexpr (FWD) v[j] += w;
+            else v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w));
+        }
+    }
+    const int col = GLU ? 16 * (et >> 5) + (lane & 15) : FWD ? et : (et & ~7) | ((et & 7) >> 1) | ((et & 1) << 2);
+    const int n = (tile / tiles_m) * TILE_ROWS + rank * COLS + col;
+    const bool n_ok = n < p.N;
+    const bool up = GLU && lane >= 16;
+    float rsw = 1.0f, bias = 0.0f;
+    if constexpr (FWD) {
+        const Proj &w = up ? p.b : p.a;
+        rsw = n_ok ? __frcp_rn(ld_dep(w.sw + n)) * 0.0625f : 1.0f;
+        bias = n_ok && w.bias ? ld_dep(w.bias + n) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const int m = m0 + j;
+        if (m >= p.M) break;
+        const float t = ld_dep(p.tok + m);
+        float y;
+        if constexpr (FWD) {
+            const float z = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[j]), __frcp_rn(t)), rsw) + bias;
+            const float other = GLU ? __shfl_xor_sync(0xffffffffu, z, 16) : 0.0f;
+            if (up || !n_ok) continue;
+            y = act_any(p.act, z);
+            if constexpr (GLU) y *= other;
+            else if (p.e.R) y += ld_elem(static_cast<const T *>(p.e.R) + (size_t)m * p.e.ldr + n);
+            if (p.e.Z) {
+                st_elem(static_cast<T *>(p.e.Z) + (size_t)m * p.e.ldz + n, z);
+                if constexpr (GLU) st_elem(static_cast<T *>(p.e.U) + (size_t)m * p.e.ldz + n, other);
+            }
+        } else {
+            if (!n_ok) continue;
+            y = __uint_as_float(v[j]) * t;
+        }
+        st_elem(static_cast<T *>(p.e.Y) + (size_t)m * p.e.ldy + n, y);
+    }
+}
+
 // ------------------------------------------------------------- host side ---
+
+// CTA pairs of a launch: one per two of the B200's 148 SMs. A property of the
+// plan (the partial tiles' slots depend on it), not of the device at hand:
+// with fewer SMs the pairs run one after another, none waits for another.
+constexpr int PAIRS = 74;
+
+// Token tile and sharing of a call, by estimated time: rounds of whole tiles,
+// or equal runs of stages plus the join. Measured per stage of 8 MMAs: about
+// 760 ns with 256 tokens (1.0 us the two-plane forms' stage of the same
+// length is included), 480 with 128, 400 with 64; the last tile's epilogue
+// about 5 us per 256 tokens; the join about 3 us and the partial tiles' two
+// passes at 4 TB/s.
+struct PairPlan {
+    int nt;
+    bool split;
+    size_t part_bytes;
+};
+inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages) {
+    PairPlan best = {256, false, 0};
+    double best_t = -1.0;
+    const int cand[3] = {256, 128, 64};
+    const double stage_ns[3] = {760.0, 480.0, 400.0};
+    for (int i = 0; i < 3; ++i) {
+        const int nt = cand[i];
+        const long long tiles = (long long)((M + nt - 1) / nt) * ((rows + tile_rows - 1) / tile_rows);
+        const double whole = (double)((tiles + PAIRS - 1) / PAIRS) * stages * stage_ns[i] + 20.0 * nt;
+        if (best_t < 0 || whole < best_t) {
+            best_t = whole;
+            best = {nt, false, 0};
+        }
+        const size_t slot = (size_t)256 * nt * 4;
+        const double share = (double)((tiles * stages + PAIRS - 1) / PAIRS) * stage_ns[i] + 20.0 * nt + 3000.0 +
+                             2.0 * PAIRS * slot / 2000.0;
+        if (tiles * stages >= PAIRS && share < best_t) {
+            best_t = share;
+            best = {nt, true, 2 * PAIRS * slot};
+        }
+    }
+    return best;
+}
+// Stages of a call: forward 256 k, gradient 128 n (64 for two planes) per segment.
+inline PairPlan forward_plan(int M, int K, int N, bool glu) { return pair_plan(M, N, glu ? 128 : 256, (K + 255) / 256); }
+inline PairPlan grad_plan(int M, int K, int segs, int seg, bool two) {
+    return pair_plan(M, K, 256, segs * (seg / (two ? 64 : 128)));
+}
 
 // What a launch needs beside PairArgs: the operands' shapes.
 struct PairCall {
@@ -711,7 +925,6 @@ struct PairCall {
     int w_rows, ldp;             // packed rows and their stride
     const void *X;               // INT8 rows [M][ldq], or FP16 rows [planes M][width]
     int x_rows, x_inner;         // rows and row elements (= stride) of X
-    int sm_count;
 };
 
 template <int MODE, int NT, typename T>
@@ -763,36 +976,20 @@ w4a8_status launch_pair(PairArgs p, const PairCall &c, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     const long long tiles = (long long)((p.M + NT - 1) / NT) * ((p.N + TILE_ROWS - 1) / TILE_ROWS);
-    const long long pairs = tiles < c.sm_count / 2 ? tiles : c.sm_count / 2;
+    const long long pairs = p.parts || tiles > PAIRS ? PAIRS : tiles;
     cfg.gridDim = dim3((unsigned)(2 * pairs));
-    return from_cuda(cudaLaunchKernelEx(&cfg, kern, wa, wb, x, out[0], out[1], out[2], p));
-}
-
-// Token tile: the one with the least rounds of tiles times the cost of a
-// stage, where an MMA stage takes 2 NT tensor cycles (twice for two planes)
-// and the widening about 400 whatever the tile.
-inline int pick_pair_tile(int M, int rows, int tile_rows, int planes, int sm_count) {
-    const int cand[3] = {256, 128, 64};
-    int best = 256;
-    long long best_cost = -1;
-    for (int nt : cand) {
-        const long long tiles = (long long)((M + nt - 1) / nt) * ((rows + tile_rows - 1) / tile_rows);
-        const long long rounds = (tiles + sm_count / 2 - 1) / (sm_count / 2);
-        const long long mma = 2LL * nt * planes;
-        const long long cost = rounds * (mma > 400 ? mma : 400);
-        if (best_cost < 0 || cost < best_cost) {
-            best_cost = cost;
-            best = nt;
-        }
-    }
-    return best;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, wa, wb, x, out[0], out[1], out[2], p);
+    if (e == cudaSuccess && p.parts)
+        e = launch_pdl(k_mlp_join<MODE, NT, T>, dim3(PAIRS - 1, (unsigned)((p.M < NT ? p.M : NT) + UNIT - 1) / UNIT),
+                       dim3(256), 0, stream, p, PAIRS);
+    return from_cuda(e);
 }
 
 template <int MODE, typename T>
-w4a8_status launch_pair_any(const PairArgs &p, const PairCall &c, cudaStream_t s) {
-    const int nt = pick_pair_tile(p.M, p.N, MODE == FWD_GLU ? 128 : 256, Shape<MODE, 64>::PLANES, c.sm_count);
-    if (nt == 256) return launch_pair<MODE, 256, T>(p, c, s);
-    if (nt == 128) return launch_pair<MODE, 128, T>(p, c, s);
+w4a8_status launch_pair_any(const PairPlan &plan, PairArgs p, const PairCall &c, void *parts, cudaStream_t s) {
+    p.parts = plan.split ? static_cast<uint32_t *>(parts) : nullptr;
+    if (plan.nt == 256) return launch_pair<MODE, 256, T>(p, c, s);
+    if (plan.nt == 128) return launch_pair<MODE, 128, T>(p, c, s);
     return launch_pair<MODE, 64, T>(p, c, s);
 }
 
