@@ -481,59 +481,76 @@ def w4g_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor, s
 # float32 or all bfloat16; act is "none", "relu", "silu", "gelu" or
 # "gelu_tanh". Formulas and rules: include/w4a8.h.
 
-def _io_flags(rows: torch.Tensor, act: str, path: str, static_weights: bool):
+# A call on few rows takes the GPU about as long as its marshalling takes the
+# host, so this part keeps to plain integers and checks each fact once.
+
+def _mlp_flags(rows: torch.Tensor, act: str, path: str, static_weights: bool):
     """(flags, activation code) of a call on rows of this type."""
-    if rows.dtype not in _IO:
-        raise ValueError("rows must be float32 or bfloat16")
-    if act not in _ACT:
-        raise ValueError(f"act must be one of {', '.join(_ACT)}")
-    return _IO[rows.dtype] | _PATH[path] | (STATIC_WEIGHTS if static_weights else 0), _ACT[act]
-
-
-def _io_rows(t: torch.Tensor | None, name: str, like: torch.Tensor, m: int, n: int) -> int:
-    """Row stride of an [m][n] tensor of like's dtype and device (0 for None)."""
-    if t is None:
-        return 0
-    if t.dtype != like.dtype or t.device != like.device or tuple(t.shape) != (m, n):
-        raise ValueError(f"{name} must be a [{m}][{n}] {like.dtype} tensor on {like.device}")
-    return _row_stride(t, name)
+    try:
+        return _IO[rows.dtype] | _PATH[path] | (STATIC_WEIGHTS if static_weights else 0), _ACT[act]
+    except KeyError as e:
+        raise ValueError(f"rows must be float32 or bfloat16, act one of {', '.join(_ACT)}, path one of "
+                         f"{', '.join(_PATH)}; got {e}") from None
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
-    # torch gives no meaning to the stride of a single row or column
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    """Row stride of a 2-D tensor with unit column stride. torch gives no
+    meaning to the stride of a single row or column."""
+    ld, one = t.stride()
+    rows, cols = t.shape
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return ld if rows > 1 else max(ld, cols)
 
 
-def _weights(k: int, like: torch.Tensor, **named):
-    """Checks packed codes [N][ldp >= packed_ld(k)] and float32 vectors [N]; returns (N, ldp)."""
-    n = ldp = None
-    for name, t in named.items():
-        if t is None:
-            continue
-        if t.device != like.device:
-            raise ValueError(f"{name} must be on {like.device}")
-        if t.dtype == torch.uint8:
-            if t.dim() != 2 or t.shape[1] < packed_ld(k):
-                raise ValueError(f"{name} must be [N][>= {packed_ld(k)}] packed codes for K = {k}")
-            ld = _row_stride(t, name)
-            if ldp is not None and (ld != ldp or t.shape[0] != n):
-                raise ValueError("the two projections must have the same shape and row stride")
-            n, ldp = t.shape[0], ld
-        elif t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
-            raise ValueError(f"{name} must be a contiguous float32 tensor of {n} values")
-    if n is None:
-        raise ValueError("packed codes must be uint8")
-    return n, ldp
+def _like(t: torch.Tensor | None, name: str, dtype, device, shape) -> int:
+    """Row stride of an optional row tensor of this type, device and shape (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or t.device != device or t.shape != shape:
+        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on {device}")
+    return _row_stride(t, name)
 
 
-def _space(workspace, need: int, like: torch.Tensor):
+def _codes(wp: torch.Tensor, name: str, k: int, device):
+    """(N, row stride) of packed codes [N][>= packed_ld(k)]."""
+    if wp.dtype != torch.uint8 or wp.device != device or wp.dim() != 2 or wp.shape[1] < (k + 1) // 2:
+        raise ValueError(f"{name} must be [N][>= {packed_ld(k)}] packed uint8 codes for K = {k} on {device}")
+    return wp.shape[0], _row_stride(wp, name)
+
+
+def _vector(t: torch.Tensor | None, name: str, n: int, device) -> int | None:
+    """Address of a float32 vector of n values (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.device != device or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} values on {device}")
+    return t.data_ptr()
+
+
+def _at(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _two_dim(t: torch.Tensor, name: str):
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    return t.shape
+
+
+def _mlp_call(fn, what: str, device, size, args, workspace, stream):
+    """fn(*args, workspace, bytes, stream) with the rows' device current."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _mlp_call(fn, what, device, size, args, workspace, stream)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
-    elif workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {like.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+        workspace = torch.empty(max(size(), 1), dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    status = fn(*args, workspace.data_ptr(), workspace.nbytes, s)
+    if status != OK:
+        raise W4A8Error(status, what)
 
 
 def act_workspace_size(m: int, k: int, n: int, projections: int = 1, dtype=torch.float32) -> int:
@@ -551,18 +568,21 @@ def w4a8_linear_act(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, bias: t
     """Y[M][N] = act(dequant(quant8(X) @ unpack(Wp)^T) + bias) + residual, of
     X's dtype. With save (or z given) returns (Y, Z), Z the pre-activations
     that w4a8_linear_act_grad reads. y may be the residual itself."""
-    flags, fn = _io_flags(x, act, path, static_weights)
-    ldx = _row_stride(x, "X")
-    m, k = x.shape
-    n, ldp = _weights(k, x, wp=wp, sw=sw, bias=bias)
-    y = torch.empty((m, n), dtype=x.dtype, device=x.device) if y is None else y
-    z = torch.empty((m, n), dtype=x.dtype, device=x.device) if save and z is None else z
-    ldy, ldz, ldr = (_io_rows(t, nm, x, m, n) for t, nm in ((y, "Y"), (z, "Z"), (residual, "residual")))
-    with torch.cuda.device(x.device):
-        ws, wsb = _space(workspace, act_workspace_size(m, k, n, 1, x.dtype), x)
-        _check(lib.w4a8_linear_act(_ptr(x), m, k, ldx, _ptr(wp), ldp, _ptr(sw), n, _ptr(bias), fn,
-                                   _ptr(residual), ldr, flags, _ptr(y), ldy, _ptr(z), ldz, _ptr(ws), wsb,
-                                   _stream(stream)), "w4a8_linear_act")
+    flags, code = _mlp_flags(x, act, path, static_weights)
+    m, k = _two_dim(x, "X")
+    dt, dev = x.dtype, x.device
+    n, ldp = _codes(wp, "wp", k, dev)
+    if y is None:
+        y = torch.empty((m, n), dtype=dt, device=dev)
+    if save and z is None:
+        z = torch.empty((m, n), dtype=dt, device=dev)
+    shape = (m, n)
+    ldy, ldz, ldr = (_like(y, "Y", dt, dev, shape), _like(z, "Z", dt, dev, shape),
+                     _like(residual, "residual", dt, dev, shape))
+    _mlp_call(lib.w4a8_linear_act, "w4a8_linear_act", dev, lambda: act_workspace_size(m, k, n, 1, dt),
+              (x.data_ptr(), m, k, _row_stride(x, "X"), wp.data_ptr(), ldp, _vector(sw, "sw", n, dev), n,
+               _vector(bias, "bias", n, dev), code, _at(residual), ldr, flags, y.data_ptr(), ldy, _at(z), ldz),
+              workspace, stream)
     return y if z is None else (y, z)
 
 
@@ -574,22 +594,30 @@ def w4a8_glu(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, wu: torch.Tens
     """H[M][N] = act(G) * U of X's dtype, G and U the gate and up projections
     of X with their biases. With save (or g and u given) returns (H, G, U) for
     w4a8_glu_grad."""
-    flags, fn = _io_flags(x, act, path, static_weights)
-    ldx = _row_stride(x, "X")
-    m, k = x.shape
-    n, ldp = _weights(k, x, wg=wg, wu=wu, sg=sg, su=su, gate_bias=gate_bias, up_bias=up_bias)
-    h = torch.empty((m, n), dtype=x.dtype, device=x.device) if h is None else h
+    flags, code = _mlp_flags(x, act, path, static_weights)
+    m, k = _two_dim(x, "X")
+    dt, dev = x.dtype, x.device
+    n, ldp = _pair(wg, wu, k, dev)
+    if h is None:
+        h = torch.empty((m, n), dtype=dt, device=dev)
     if save and g is None and u is None:
-        g, u = (torch.empty((m, n), dtype=x.dtype, device=x.device) for _ in range(2))
-    ldh, ldg, ldu = (_io_rows(t, nm, x, m, n) for t, nm in ((h, "H"), (g, "G"), (u, "U")))
+        g, u = (torch.empty((m, n), dtype=dt, device=dev) for _ in range(2))
+    ldh, ldg, ldu = (_like(h, "H", dt, dev, (m, n)), _like(g, "G", dt, dev, (m, n)), _like(u, "U", dt, dev, (m, n)))
     if ldg != ldu:
         raise ValueError("G and U must both be given, with one row stride")
-    with torch.cuda.device(x.device):
-        ws, wsb = _space(workspace, act_workspace_size(m, k, n, 2, x.dtype), x)
-        _check(lib.w4a8_glu(_ptr(x), m, k, ldx, _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su), ldp, n, _ptr(gate_bias),
-                            _ptr(up_bias), fn, flags, _ptr(h), ldh, _ptr(g), _ptr(u), ldg, _ptr(ws), wsb,
-                            _stream(stream)), "w4a8_glu")
+    _mlp_call(lib.w4a8_glu, "w4a8_glu", dev, lambda: act_workspace_size(m, k, n, 2, dt),
+              (x.data_ptr(), m, k, _row_stride(x, "X"), wg.data_ptr(), _vector(sg, "sg", n, dev), wu.data_ptr(),
+               _vector(su, "su", n, dev), ldp, n, _vector(gate_bias, "gate_bias", n, dev),
+               _vector(up_bias, "up_bias", n, dev), code, flags, h.data_ptr(), ldh, _at(g), _at(u), ldg),
+              workspace, stream)
     return h if g is None else (h, g, u)
+
+
+def _pair(wg, wu, k: int, dev):
+    n, ldp = _codes(wg, "wg", k, dev)
+    if _codes(wu, "wu", k, dev) != (n, ldp):
+        raise ValueError("the two projections must have the same shape and row stride")
+    return n, ldp
 
 
 def w4a8_linear_act_grad(dy: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, k: int, act: str = "none",
@@ -599,22 +627,21 @@ def w4a8_linear_act_grad(dy: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, k
     """dX[M][k] (and with bias_grad dbias[N]) of w4a8_linear_act, of dY's
     dtype; z is the saved pre-activations (not needed without activation).
     The residual's gradient is dY."""
-    flags, fn = _io_flags(dy, act, path, static_weights)
-    lddy = _row_stride(dy, "dY")
-    m = dy.shape[0]
-    n, ldp = _weights(k, dy, wp=wp, sw=sw)
-    if dy.shape[1] != n:
-        raise ValueError(f"dY must have {n} columns")
+    flags, code = _mlp_flags(dy, act, path, static_weights)
+    m, n = _two_dim(dy, "dY")
+    dt, dev = dy.dtype, dy.device
+    rows, ldp = _codes(wp, "wp", k, dev)
+    if rows != n:
+        raise ValueError(f"dY must have {rows} columns")
     if act == "none":
         z = None
-    dx = torch.empty((m, k), dtype=dy.dtype, device=dy.device) if dx is None else dx
-    ldz, lddx = _io_rows(z, "Z", dy, m, n), _io_rows(dx, "dX", dy, m, k)
-    db = torch.empty(n, dtype=torch.float32, device=dy.device) if bias_grad else None
-    with torch.cuda.device(dy.device):
-        ws, wsb = _space(workspace, grad_workspace_size(m, k, n, 1, dy.dtype), dy)
-        _check(lib.w4a8_linear_act_grad(_ptr(dy), m, n, lddy, _ptr(z), ldz, _ptr(wp), ldp, _ptr(sw), k, fn,
-                                        flags, _ptr(dx), lddx, _ptr(db), _ptr(ws), wsb, _stream(stream)),
-               "w4a8_linear_act_grad")
+    if dx is None:
+        dx = torch.empty((m, k), dtype=dt, device=dev)
+    ldz, lddx = _like(z, "Z", dt, dev, (m, n)), _like(dx, "dX", dt, dev, (m, k))
+    db = torch.empty(n, dtype=torch.float32, device=dev) if bias_grad else None
+    _mlp_call(lib.w4a8_linear_act_grad, "w4a8_linear_act_grad", dev, lambda: grad_workspace_size(m, k, n, 1, dt),
+              (dy.data_ptr(), m, n, _row_stride(dy, "dY"), _at(z), ldz, wp.data_ptr(), ldp,
+               _vector(sw, "sw", n, dev), k, code, flags, dx.data_ptr(), lddx, _at(db)), workspace, stream)
     return (dx, db) if bias_grad else dx
 
 
@@ -624,22 +651,22 @@ def w4a8_glu_grad(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, wg: torch.
                   stream=None, static_weights: bool = False):
     """dX[M][k] (and with bias_grad the two bias gradients [N]) of w4a8_glu,
     of dH's dtype, from the saved G and U."""
-    flags, fn = _io_flags(dh, act, path, static_weights)
-    lddh = _row_stride(dh, "dH")
-    m = dh.shape[0]
-    n, ldp = _weights(k, dh, wg=wg, wu=wu, sg=sg, su=su)
-    if dh.shape[1] != n:
-        raise ValueError(f"dH must have {n} columns")
-    dx = torch.empty((m, k), dtype=dh.dtype, device=dh.device) if dx is None else dx
-    ldg, ldu, lddx = _io_rows(g, "G", dh, m, n), _io_rows(u, "U", dh, m, n), _io_rows(dx, "dX", dh, m, k)
-    if ldg != ldu:
+    flags, code = _mlp_flags(dh, act, path, static_weights)
+    m, n = _two_dim(dh, "dH")
+    dt, dev = dh.dtype, dh.device
+    rows, ldp = _pair(wg, wu, k, dev)
+    if rows != n:
+        raise ValueError(f"dH must have {rows} columns")
+    if dx is None:
+        dx = torch.empty((m, k), dtype=dt, device=dev)
+    ldg, ldu, lddx = (_like(g, "G", dt, dev, (m, n)), _like(u, "U", dt, dev, (m, n)), _like(dx, "dX", dt, dev, (m, k)))
+    if ldg != ldu or g is None:
         raise ValueError("G and U must both be given, with one row stride")
-    dbg, dbu = (torch.empty(n, dtype=torch.float32, device=dh.device) if bias_grad else None for _ in range(2))
-    with torch.cuda.device(dh.device):
-        ws, wsb = _space(workspace, grad_workspace_size(m, k, n, 2, dh.dtype), dh)
-        _check(lib.w4a8_glu_grad(_ptr(dh), m, n, lddh, _ptr(g), _ptr(u), ldg, _ptr(wg), _ptr(sg), _ptr(wu), _ptr(su),
-                                 ldp, k, fn, flags, _ptr(dx), lddx, _ptr(dbg), _ptr(dbu), _ptr(ws), wsb,
-                                 _stream(stream)), "w4a8_glu_grad")
+    dbg, dbu = (torch.empty(n, dtype=torch.float32, device=dev) if bias_grad else None for _ in range(2))
+    _mlp_call(lib.w4a8_glu_grad, "w4a8_glu_grad", dev, lambda: grad_workspace_size(m, k, n, 2, dt),
+              (dh.data_ptr(), m, n, _row_stride(dh, "dH"), g.data_ptr(), u.data_ptr(), ldg, wg.data_ptr(),
+               _vector(sg, "sg", n, dev), wu.data_ptr(), _vector(su, "su", n, dev), ldp, k, code, flags,
+               dx.data_ptr(), lddx, _at(dbg), _at(dbu)), workspace, stream)
     return (dx, dbg, dbu) if bias_grad else dx
 
 
