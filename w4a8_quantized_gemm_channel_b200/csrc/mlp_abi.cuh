@@ -88,7 +88,8 @@ w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a
     if (path != W4A8_PATH_GENERIC && path != W4A8_PATH_DECODE && path != W4A8_PATH_TC) return W4A8_ERR_UNSUPPORTED;
     if (path == W4A8_PATH_DECODE && !dec.ok) return W4A8_ERR_UNSUPPORTED;
     if (path != W4A8_PATH_GENERIC && tc::encode_fn() == nullptr) return W4A8_ERR_UNSUPPORTED;
-    const bool fused = path == W4A8_PATH_DECODE && dec.units > 0;
+    const bool fused = path == W4A8_PATH_DECODE ? dec.units > 0
+                                                : path == W4A8_PATH_GENERIC && K <= mlp::SIMT_FUSED_K;
     w4a8_status st = W4A8_OK;
     if (!fused) st = launch_quant_rows<T>(X, M, K, ldx, ws, flags, s);
     if (st != W4A8_OK) return st;
@@ -118,12 +119,14 @@ w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a
     }
     st = by_act(act, [&](auto A) {
         const dim3 grid((N + 127) / 128, M < 65535 ? M : 65535);
-        return from_cuda(launch_pdl(mlp::k_mlp_simt<GLU, decltype(A)::value, T>, grid, dim3(128), 0, s, ws.xq, M, K,
-                                    ws.ldq, ws.sx, a, b, ldp, N, ea));
+        auto kern = fused ? mlp::k_mlp_simt<GLU, true, decltype(A)::value, T>
+                          : mlp::k_mlp_simt<GLU, false, decltype(A)::value, T>;
+        return from_cuda(launch_pdl(kern, grid, dim3(128), 0, s, static_cast<const T *>(X), ldx,
+                                    (int)io_vec(X, ldx, flags), ws.xq, M, K, ws.ldq, ws.sx, a, b, ldp, N, ea));
     });
     if (st != W4A8_OK) return st;
     t_last_path = W4A8_PATH_GENERIC;
-    t_last_launches = 2;
+    t_last_launches = fused ? 1 : 2;
     t_last_kernel = "k_mlp_simt";
     return W4A8_OK;
 }
@@ -190,17 +193,22 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
         constexpr int ACT = decltype(A)::value;
         if (dba || dbb) {
             const int slices = (M + mlp::BG_ROWS - 1) / mlp::BG_ROWS;
-            if (slices > 65535) return (w4a8_status)W4A8_ERR_UNSUPPORTED;
-            cudaError_t e = launch_pdl(mlp::k_bias_grad_part<GLU, ACT, T>, dim3((N + 31) / 32, slices), dim3(256), 0,
-                                       s, in, M, ws.part);
+            cudaError_t e = launch_pdl(mlp::k_bias_grad_part<GLU, ACT, T>,
+                                       dim3((N + 255) / 256, slices < 65535 ? slices : 65535), dim3(256), 0, s, in, M,
+                                       ws.part);
             if (e != cudaSuccess) return (w4a8_status)W4A8_ERR_CUDA;
             e = launch_pdl(mlp::k_bias_grad_sum, dim3((N + 255) / 256, SEGS), dim3(256), 0, s,
                            (const float *)ws.part, slices, SEGS, N, dba, dbb);
             if (e != cudaSuccess) return (w4a8_status)W4A8_ERR_CUDA;
             launches += 2;
         }
-        return from_cuda(launch_pdl(mlp::k_grad_rows<GLU, LO, ACT, T>, dim3(M < 65535 ? M : 65535),
-                                    dim3(mlp::GR_THREADS), 0, s, in, M, ws.seg, ws.P, ws.rs));
+        const int bytes = SEGS * ws.seg * (int)sizeof(float);
+        const bool held = bytes <= mlp::GR_HELD_MAX;
+        auto kern = held ? mlp::k_grad_rows<GLU, LO, true, ACT, T> : mlp::k_grad_rows<GLU, LO, false, ACT, T>;
+        if (held && !raise_smem_limit(reinterpret_cast<const void *>(kern), mlp::GR_HELD_MAX))
+            return (w4a8_status)W4A8_ERR_CUDA;
+        return from_cuda(launch_pdl(kern, dim3(M < 65535 ? M : 65535), dim3(mlp::GR_THREADS), held ? bytes : 0, s, in,
+                                    M, ws.seg, ws.P, ws.rs));
     });
     if (st != W4A8_OK) return st;
     if (path == W4A8_PATH_TC) {
@@ -247,7 +255,9 @@ w4a8_status mlp_grad_call(const void *dY, int M, int N, int lddy, const void *Z,
     auto run = [&](auto elem) {
         using T = decltype(elem);
         const mlp::GradIn<GLU, T> in = {static_cast<const T *>(dY), static_cast<const T *>(Z),
-                                        static_cast<const T *>(U), sa, sb, N, lddy, ldz};
+                                        static_cast<const T *>(U), sa, sb, N, lddy, ldz,
+                                        io_vec(dY, lddy, flags) && (!Z || io_vec(Z, ldz, flags)) &&
+                                            (!U || io_vec(U, ldz, flags))};
         return mlp_grad<GLU, T>(in, M, Wa, Wb, ldp, K, act, flags, dX, lddx, dba, dbb, ws, s);
     };
     return io_bf16(flags) ? run(__nv_bfloat16()) : run(float());

@@ -216,22 +216,23 @@ struct GradIn {
     const T *z, *u;   // [M][ldz]: saved pre-activations (z: gate, or the linear's z; null without activation)
     const float *sw, *su;
     int N, lddy, ldz;
-    // the segments' values of column n in row m, before the scales
+    int vec;          // the rows' eight-element pieces are 16-byte aligned
+    // the segments' values of columns n..n+7 in row m, before the scales; zeros past N
     template <int ACT>
-    __device__ __forceinline__ void dz(int m, int n, float &a, float &b) const {
-        const float dyv = ld_elem(dy + (size_t)m * lddy + n);
-        if constexpr (GLU) {
-            float av, dv;
-            act_value_grad<ACT>(ld_elem(z + (size_t)m * ldz + n), av, dv);
-            a = dyv * ld_elem(u + (size_t)m * ldz + n) * dv;
-            b = dyv * av;
-        } else {
-            b = 0.0f;
-            a = dyv;
-            if constexpr (ACT != W4A8_ACT_NONE) {
+    __device__ __forceinline__ void dz8(int m, int n, float (&a)[8], float (&b)[8]) const {
+        float d[8], g[8], w[8];
+        ld_row8(dy + (size_t)m * lddy, n, N, vec != 0, d);
+        if (GLU || ACT != W4A8_ACT_NONE) ld_row8(z + (size_t)m * ldz, n, N, vec != 0, g);
+        if constexpr (GLU) ld_row8(u + (size_t)m * ldz, n, N, vec != 0, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            a[i] = d[i];
+            b[i] = 0.0f;
+            if constexpr (GLU || ACT != W4A8_ACT_NONE) {
                 float av, dv;
-                act_value_grad<ACT>(ld_elem(z + (size_t)m * ldz + n), av, dv);
-                a = dyv * dv;
+                act_value_grad<ACT>(g[i], av, dv);
+                a[i] = GLU ? d[i] * w[i] * dv : d[i] * dv;
+                if constexpr (GLU) b[i] = d[i] * av;
             }
         }
     }
@@ -247,38 +248,83 @@ __device__ __forceinline__ void row_power(float amax, float &s, float &rs) {
     rs = __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
-constexpr int GR_THREADS = 256;
+// One block per row: the values go to shared memory as float32 while the
+// row's abs-max is taken, then out as FP16. (HELD false: rows whose values do
+// not fit are computed twice.) v = dz / sw by a fast reciprocal, 2 ulp. Bound:
+// HBM, (1 + saved) N T read and 2 N bytes per segment and plane written.
+constexpr int GR_THREADS = 512;
+constexpr int GR_HELD_MAX = 220 * 1024;  // bytes of values a block may hold
 
-template <bool GLU, bool LO, int ACT, typename T>
+template <bool GLU, bool LO, bool HELD, int ACT, typename T>
 __global__ void __launch_bounds__(GR_THREADS)
 k_grad_rows(GradIn<GLU, T> in, int M, int seg, __half *__restrict__ P, float *__restrict__ rs) {
     __shared__ float red[GR_THREADS / 32];
+    extern __shared__ __align__(16) float held[];  // HELD: [segments][seg]
     griddep_wait();
     griddep_launch_dependents();
     const int width = GLU ? 2 * seg : seg;
+    // v of columns n..n+7: dz / sw
+    auto values = [&](int m, int n, float (&a)[8], float (&b)[8]) {
+        in.template dz8<ACT>(m, n, a, b);
+        float s[8];
+        ld_row8(in.sw, n, in.N, (reinterpret_cast<uintptr_t>(in.sw) & 15) == 0, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = n + i < in.N ? __fdividef(a[i], s[i]) : 0.0f;
+        if constexpr (GLU) {
+            ld_row8(in.su, n, in.N, (reinterpret_cast<uintptr_t>(in.su) & 15) == 0, s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = n + i < in.N ? __fdividef(b[i], s[i]) : 0.0f;
+        }
+    };
+    auto keep = [&](int i, const float (&v)[8]) {
+        *reinterpret_cast<float4 *>(held + i) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(held + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    };
+    auto kept = [&](int i, float (&v)[8]) {
+        const float4 x = *reinterpret_cast<const float4 *>(held + i), y = *reinterpret_cast<const float4 *>(held + i + 4);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    };
     for (int m = blockIdx.x; m < M; m += gridDim.x) {
         float amax = 0.0f;
-        for (int n = threadIdx.x; n < in.N; n += GR_THREADS) {
-            float a, b;
-            in.template dz<ACT>(m, n, a, b);
-            amax = fmaxf(amax, fabsf(__fdiv_rn(a, ld_dep(in.sw + n))));
-            if constexpr (GLU) amax = fmaxf(amax, fabsf(__fdiv_rn(b, ld_dep(in.su + n))));
+        for (int n = 8 * threadIdx.x; n < seg; n += 8 * GR_THREADS) {
+            float a[8], b[8];
+            values(m, n, a, b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                amax = fmaxf(amax, fabsf(a[i]));
+                if constexpr (GLU) amax = fmaxf(amax, fabsf(b[i]));
+            }
+            if constexpr (HELD) {
+                keep(n, a);
+                if constexpr (GLU) keep(seg + n, b);
+            }
         }
         float s, r;
         row_power(block_max<GR_THREADS>(amax, red), s, r);
         if (threadIdx.x == 0) rs[m] = r;
         __half *hi = P + (size_t)m * width, *lo = hi + (size_t)M * width;
-        auto put = [&](int i, float v) {
-            const __half h = __float2half_rn(v);
-            hi[i] = h;
-            if constexpr (LO) lo[i] = __float2half_rn(v - __half2float(h));
+        auto put = [&](int i, const float (&v)[8]) {
+            __half2 h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = v[2 * j] * s, y = v[2 * j + 1] * s;
+                h[j] = __floats2half2_rn(x, y);
+                if constexpr (LO) {
+                    const float2 f = __half22float2(h[j]);
+                    l[j] = __floats2half2_rn(x - f.x, y - f.y);
+                }
+            }
+            *reinterpret_cast<uint4 *>(hi + i) = *reinterpret_cast<const uint4 *>(h);
+            if constexpr (LO) *reinterpret_cast<uint4 *>(lo + i) = *reinterpret_cast<const uint4 *>(l);
         };
-        for (int n = threadIdx.x; n < seg; n += GR_THREADS) {
-            float a = 0.0f, b = 0.0f;
-            if (n < in.N) {
-                in.template dz<ACT>(m, n, a, b);
-                a = __fdiv_rn(a, ld_dep(in.sw + n)) * s;
-                if constexpr (GLU) b = __fdiv_rn(b, ld_dep(in.su + n)) * s;
+        for (int n = 8 * threadIdx.x; n < seg; n += 8 * GR_THREADS) {  // a thread's own pieces
+            float a[8], b[8];
+            if constexpr (HELD) {
+                kept(n, a);
+                if constexpr (GLU) kept(seg + n, b);
+            } else {
+                values(m, n, a, b);
             }
             put(n, a);
             if constexpr (GLU) put(seg + n, b);
@@ -286,39 +332,51 @@ k_grad_rows(GradIn<GLU, T> in, int M, int seg, __half *__restrict__ P, float *__
     }
 }
 
-// Bias gradients: column sums of dz. Block (column block of 32, row slice):
-// each of 8 warps adds every eighth row of the slice, the warps' sums meet in
-// shared memory in a fixed order, and a second kernel adds the slices in
-// order, so a run repeats bit for bit. Sums are float32 over at most
-// BG_ROWS / 8 rows, then 8, then the slices.
-constexpr int BG_ROWS = 256;
+// Bias gradients: column sums of dz. Block (256 columns, row slice): each of 8
+// warps adds every eighth row of the slice, eight columns per lane, the warps'
+// sums meet in shared memory in a fixed order, and a second kernel adds the
+// slices in order, so a run repeats bit for bit. Sums are float32 over at most
+// BG_ROWS / 8 rows, then 8, then the slices. Bound: HBM, the rows read once more.
+constexpr int BG_ROWS = 64;
 
 template <bool GLU, int ACT, typename T>
 __global__ void __launch_bounds__(256)
 k_bias_grad_part(GradIn<GLU, T> in, int M, float *__restrict__ part) {
-    __shared__ float red[GLU ? 2 : 1][8][33];
+    constexpr int SEGS = GLU ? 2 : 1;
+    __shared__ float red[SEGS][8][256];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n = blockIdx.x * 32 + lane;
-    const int m1 = min(M, ((int)blockIdx.y + 1) * BG_ROWS);
-    float sa = 0.0f, sb = 0.0f;
-    if (n < in.N) {
-        for (int m = blockIdx.y * BG_ROWS + warp; m < m1; m += 8) {
-            float a, b;
-            in.template dz<ACT>(m, n, a, b);
-            sa += a;
-            sb += b;
-        }
-    }
-    red[0][warp][lane] = sa;
-    if constexpr (GLU) red[1][warp][lane] = sb;
-    __syncthreads();
-    if (warp < (GLU ? 2 : 1) && n < in.N) {
-        float t = 0.0f;
+    const int n0 = blockIdx.x * 256, n = n0 + 8 * lane;
+    for (int slice = blockIdx.y; slice * BG_ROWS < M; slice += gridDim.y) {
+        const int m1 = min(M, (slice + 1) * BG_ROWS);
+        float sa[8] = {}, sb[8] = {};
+        if (n < in.N) {
+#pragma unroll 2
+            for (int m = slice * BG_ROWS + warp; m < m1; m += 8) {
+                float a[8], b[8];
+                in.template dz8<ACT>(m, n, a, b);
 #pragma unroll
-        for (int w = 0; w < 8; ++w) t += red[warp][w][lane];
-        part[((size_t)blockIdx.y * (GLU ? 2 : 1) + warp) * in.N + n] = t;
+                for (int i = 0; i < 8; ++i) {
+                    sa[i] += a[i];
+                    sb[i] += b[i];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            red[0][warp][8 * lane + i] = sa[i];
+            if constexpr (GLU) red[1][warp][8 * lane + i] = sb[i];
+        }
+        __syncthreads();
+        for (int s = 0; s < SEGS; ++s) {
+            const int c = threadIdx.x;
+            float t = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) t += red[s][w][c];
+            if (n0 + c < in.N) part[((size_t)slice * SEGS + s) * in.N + n0 + c] = t;
+        }
+        __syncthreads();
     }
 }
 
@@ -331,6 +389,7 @@ k_bias_grad_sum(const float *part, int slices, int segs, int N, float *dba, floa
     float *out = blockIdx.y == 0 ? dba : dbb;
     if (n >= N || out == nullptr) return;
     float t = 0.0f;
+#pragma unroll 8
     for (int s = 0; s < slices; ++s) t += ld_dep(part + ((size_t)s * segs + blockIdx.y) * N + n);
     out[n] = t;
 }

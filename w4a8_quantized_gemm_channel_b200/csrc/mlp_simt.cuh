@@ -27,38 +27,66 @@ __device__ __forceinline__ float dequant(int32_t acc, float rsx, float rsw, floa
     return __fmul_rn(__fmul_rn(__int2float_rn(acc), rsx), rsw) + b;
 }
 
-// One thread per output. Xq is in the k-permuted order, so a packed word of
-// eight codes meets two words of the row: two dp4a on sign-extended nibbles.
-template <bool GLU, int ACT, typename T>
+// One thread per output. The row is in the k-permuted order, so a packed word
+// of eight codes meets two words of it: two dp4a on sign-extended nibbles.
+// FUSED (K <= SIMT_FUSED_K): a block quantizes its row into shared memory
+// first, so a tiny call is one launch; otherwise Xq and sx are the row pass's.
+constexpr int SIMT_FUSED_K = 4096;
+
+template <bool GLU, bool FUSED, int ACT, typename T>
 __global__ void __launch_bounds__(128)
-k_mlp_simt(const int8_t *Xq, int M, int K, int ldq, const float *sx, Proj a, Proj b, int ldp, int N, EpiArgs e) {
+k_mlp_simt(const T *X, int ldx, int vec, const int8_t *Xq, int M, int K, int ldq, const float *sx, Proj a, Proj b,
+           int ldp, int N, EpiArgs e) {
+    __shared__ uint2 codes[FUSED ? SIMT_FUSED_K / 8 : 1];
+    __shared__ float red[4];
     griddep_launch_dependents();
     griddep_wait();
-    const int n = blockIdx.x * 128 + threadIdx.x;
-    if (n >= N) return;
-    const float ra = __frcp_rn(ld_dep(a.sw + n)), ba = a.bias ? ld_dep(a.bias + n) : 0.0f;
-    const float rb = GLU ? __frcp_rn(ld_dep(b.sw + n)) : 0.0f, bb = GLU && b.bias ? ld_dep(b.bias + n) : 0.0f;
-    const uint32_t *wa = reinterpret_cast<const uint32_t *>(a.Wp + (size_t)n * ldp);
-    const uint32_t *wb = GLU ? reinterpret_cast<const uint32_t *>(b.Wp + (size_t)n * ldp) : wa;
+    const int n = blockIdx.x * 128 + threadIdx.x, nn = min(n, N - 1);
+    const float ra = __frcp_rn(ld_dep(a.sw + nn)), ba = a.bias ? ld_dep(a.bias + nn) : 0.0f;
+    const float rb = GLU ? __frcp_rn(ld_dep(b.sw + nn)) : 0.0f, bb = GLU && b.bias ? ld_dep(b.bias + nn) : 0.0f;
+    const uint32_t *wa = reinterpret_cast<const uint32_t *>(a.Wp + (size_t)nn * ldp);
+    const uint32_t *wb = GLU ? reinterpret_cast<const uint32_t *>(b.Wp + (size_t)nn * ldp) : wa;
     auto ld32 = [](const uint32_t *p) {
         uint32_t v;
         asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
         return v;
     };
+    const int units = (K + 7) / 8;
     for (int m = blockIdx.y; m < M; m += gridDim.y) {
+        float s;
+        if constexpr (FUSED) {
+            const T *x = X + (size_t)m * ldx;
+            float v[8], amax = 0.0f;
+            for (int u = threadIdx.x; u < units; u += 128) {
+                ld_row8(x, 8 * u, K, vec != 0, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+            }
+            s = act_scale_from_amax(block_max<128>(amax, red));  // its barriers also end the last row's reads
+            for (int u = threadIdx.x; u < units; u += 128) {
+                if (units > 128) ld_row8(x, 8 * u, K, vec != 0, v);
+                codes[u] = row_codes8(v, s);
+            }
+            __syncthreads();
+        } else {
+            s = ld_dep(sx + m);
+        }
         const uint32_t *x = reinterpret_cast<const uint32_t *>(Xq + (size_t)m * ldq);
         int32_t ca = 0, cb = 0;
-        for (int w = 0; w < (K + 7) / 8; ++w) {
-            const int xe = (int)ld32(x + 2 * w), xo = (int)ld32(x + 2 * w + 1);
+        for (int w = 0; w < units; ++w) {
+            uint2 q;
+            if constexpr (FUSED) q = codes[w];
+            else q = make_uint2(ld32(x + 2 * w), ld32(x + 2 * w + 1));
             uint32_t lo, hi;
             unpack_s4x8(ld32(wa + w), lo, hi);
-            ca = __dp4a((int)lo, xe, __dp4a((int)hi, xo, ca));
+            ca = __dp4a((int)lo, (int)q.x, __dp4a((int)hi, (int)q.y, ca));
             if constexpr (GLU) {
                 unpack_s4x8(ld32(wb + w), lo, hi);
-                cb = __dp4a((int)lo, xe, __dp4a((int)hi, xo, cb));
+                cb = __dp4a((int)lo, (int)q.x, __dp4a((int)hi, (int)q.y, cb));
             }
         }
-        const float rx = __frcp_rn(ld_dep(sx + m));
+        if (n >= N) continue;
+        const float rx = __frcp_rn(s);
         const float z = dequant(ca, rx, ra, ba);
         float y = act_value<ACT>(z);
         if constexpr (GLU) {
