@@ -329,3 +329,38 @@ def test_offsets_past_32_bits():
         ref.check(t, w, e, what)
     native.w4a8_glu_grad(h, g, u, wg, sg, wu, su, k, dx=dx)
     ref.check(dx, *ref.glu_grad(h, g, u, qg, sg, qu, su, "silu", False)[0], "dx")
+
+
+def test_huge_finite_preactivations():
+    """Finite pre-activations of any size give finite values: the activations'
+    limits and derivatives 0 or 1."""
+    n, k = 16, 8
+    q = torch.zeros((n, k), dtype=torch.int8, device="cuda")
+    q[:, 0] = 7
+    wp, sw = ref.pack(q), torch.ones(n, device="cuda")
+    b = torch.tensor([1e30, -1e30, 1e20, -1e20, 3e4, -3e4, 200.0, -200.0] * 2, device="cuda")
+    x = torch.zeros((3, k), device="cuda")
+    for act in ACTS[1:]:
+        y, z = native.w4a8_linear_act(x, wp, sw, bias=b, act=act, save=True)
+        assert torch.equal(z, b.expand(3, n))
+        assert torch.equal(y, torch.where(b > 0, b, torch.zeros_like(b)).expand(3, n)), act
+        dx = native.w4a8_linear_act_grad(torch.ones(3, n, device="cuda"), wp, sw, k, act=act, z=z)
+        assert torch.equal(dx[:, 0], torch.full((3,), 7.0 * 8, device="cuda")) and (dx[:, 1:] == 0).all(), act
+
+
+@pytest.mark.parametrize("m,k,n,io", [(100, 1152, 333, "f32"), (500, 1152, 1000, "f32"), (500, 1152, 1000, "bf16"),
+                                      (40, 4096, 2000, "bf16"), (12, 1152, 6912, "bf16"), (1, 4096, 4096, "f32")])
+def test_many_calls_give_the_same_bits(m, k, n, io):
+    """Two hundred calls in a row, as overlapped as the stream allows, repeat
+    the first one's bits: every hand-over between the kernels' warps holds."""
+    rnd = gen(m + n)
+    (_, sg, wg), (_, su, wu) = weights(rnd, n, k), weights(rnd, n, k)
+    x, dh = rows(rnd, m, k, DT[io]), rnd(m, n, std=0.01).to(DT[io])
+    h, g, u = native.w4a8_glu(x, wg, sg, wu, su, save=True)
+    for call in (lambda: native.w4a8_glu(x, wg, sg, wu, su, static_weights=True),
+                 lambda: native.w4a8_linear_act(x, wg, sg, act="silu", residual=dh),
+                 lambda: native.w4a8_glu_grad(dh, g, u, wg, sg, wu, su, k),
+                 lambda: native.w4a8_linear_act_grad(dh, wg, sg, k, act="silu", z=g)):
+        first = call()
+        again = [call() for _ in range(200)]
+        assert all(torch.equal(first, a) for a in again)

@@ -10,48 +10,76 @@ namespace w4a8 {
 namespace mlp {
 
 // ------------------------------------------------------------- activations ---
-// Everything in float32. The logistic function is taken from
-// t = exp(-|z|) in (0, 1], so nothing overflows, and 1 - s(z) = s(-z) comes
-// without cancellation. The fast exponential is off by at most 2 + 1.173 |z|
-// ulp: some 20 ulp of s where s is still above 2^-24, less than 2^-24 absolute
-// in z s beyond. The tanh
-// form of GELU is z s(2 t(z)) by 1 + tanh(a) = 2 s(2a).
-struct Logistic {
-    float s, c;  // s(z) and 1 - s(z)
-};
-__device__ __forceinline__ Logistic logistic(float z) {
-    const float t = __expf(-fabsf(z));
-    const float r = __fdividef(1.0f, 1.0f + t);
-    const float q = t * r;
-    return z >= 0.0f ? Logistic{r, q} : Logistic{q, r};
+// Everything in float32, in few instructions: an epilogue's exponentials,
+// reciprocals and conversions share one pipe at an eighth of the ALU's rate, so
+// each activation takes one of the first two each. The hardware exponential
+// (2 ulp) of a product rounded before it is off by 2 ulp + |argument| 2^-24:
+// some 20 ulp where the activation's tail is still above 2^-24, and less than
+// 2^-24 absolute beyond.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float LOG2E = 1.4426950408889634f;
 constexpr float GELU_C = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float GELU_A = 0.044715f;
 constexpr float RSQRT_2PI = 0.3989422804014327f;
 
+// exp(-2t) = 2^(z (c1 + c2 z^2)) of the tanh form, t = sqrt(2/pi)(z + 0.044715 z^3):
+// 1 + tanh(t) = 2 / (1 + exp(-2t)).
+__device__ __forceinline__ float gelu_tanh_arg(float z) {
+    return z * __fmaf_rn(-2.0f * GELU_C * GELU_A * LOG2E, z * z, -2.0f * GELU_C * LOG2E);
+}
+
+// e = exp(-z^2 / 2) and Phi(-|z|) = e g(|z|): g(x) = erfcx(x / sqrt(2)) / 2 is
+// smooth in t = 1 / (1 + 0.3 x), here the polynomial of degree 8 in t with the
+// least relative error over 0 <= x <= 14 (5.8e-8; 7 ulp evaluated in float32),
+// found by reweighted least squares against float64 erfcx. The tail keeps its
+// relative accuracy, so z Phi(z) has no cancellation for negative z.
+__device__ __forceinline__ float normal_tail(float z, float &e) {
+    const float x = fabsf(z), t = rcp_fast(__fmaf_rn(0.3f, x, 1.0f));
+    e = exp2_fast(-0.5f * LOG2E * (x * x));
+    float g = 0.0383782896f;
+    g = __fmaf_rn(g, t, -0.169166112f);
+    g = __fmaf_rn(g, t, 0.228660081f);
+    g = __fmaf_rn(g, t, -0.0765064774f);
+    g = __fmaf_rn(g, t, 0.142535524f);
+    g = __fmaf_rn(g, t, 0.0946835229f);
+    g = __fmaf_rn(g, t, 0.121920342f);
+    g = __fmaf_rn(g, t, 0.119487689f);
+    g = __fmaf_rn(g, t, 7.168876e-06f);
+    return e * g;
+}
+
+// z / (1 + e) with e = exp(-..): an overflowing e gives the limit 0.
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
     if constexpr (ACT == W4A8_ACT_NONE) return z;
     if constexpr (ACT == W4A8_ACT_RELU) return z > 0.0f ? z : 0.0f;
-    if constexpr (ACT == W4A8_ACT_SILU) return z * logistic(z).s;
-    if constexpr (ACT == W4A8_ACT_GELU) return z * normcdff(z);
-    if constexpr (ACT == W4A8_ACT_GELU_TANH) {
-        const float t = GELU_C * __fmaf_rn(GELU_A * z * z, z, z);
-        return z * logistic(2.0f * t).s;
+    if constexpr (ACT == W4A8_ACT_SILU) return z * rcp_fast(1.0f + exp2_fast(-LOG2E * z));
+    if constexpr (ACT == W4A8_ACT_GELU) {
+        float e;
+        const float q = normal_tail(z, e);
+        return z * (z < 0.0f ? q : 1.0f - q);
     }
+    if constexpr (ACT == W4A8_ACT_GELU_TANH) return z * rcp_fast(1.0f + exp2_fast(gelu_tanh_arg(z)));
     return z;
 }
 
-// The activation by its code: for places that finish few values.
-__device__ __noinline__ float act_any(int act, float z) {
-    switch (act) {
-        case W4A8_ACT_RELU: return act_value<W4A8_ACT_RELU>(z);
-        case W4A8_ACT_SILU: return act_value<W4A8_ACT_SILU>(z);
-        case W4A8_ACT_GELU: return act_value<W4A8_ACT_GELU>(z);
-        case W4A8_ACT_GELU_TANH: return act_value<W4A8_ACT_GELU_TANH>(z);
-        default: return z;
-    }
+// s(a) and 1 - s(a) of the logistic function at a with -a log2(e) given, from
+// exp(-|a|) in (0, 1]: no overflow, and no cancellation in 1 - s.
+struct Logistic {
+    float s, c;
+};
+__device__ __forceinline__ Logistic logistic2(float minus_a_log2e) {
+    const float t = exp2_fast(-fabsf(minus_a_log2e)), r = rcp_fast(1.0f + t), q = t * r;
+    return minus_a_log2e <= 0.0f ? Logistic{r, q} : Logistic{q, r};
 }
 
 // The activation and its derivative at z (ReLU's derivative at 0 is 0).
@@ -63,18 +91,30 @@ __device__ __forceinline__ void act_value_grad(float z, float &a, float &d) {
         a = z > 0.0f ? z : 0.0f;
         d = z > 0.0f ? 1.0f : 0.0f;
     } else if constexpr (ACT == W4A8_ACT_SILU) {
-        const Logistic l = logistic(z);
+        const Logistic l = logistic2(-LOG2E * z);
         a = z * l.s;
         d = l.s * __fmaf_rn(z, l.c, 1.0f);
     } else if constexpr (ACT == W4A8_ACT_GELU) {
-        const float p = normcdff(z);
+        float e;
+        const float q = normal_tail(z, e), p = z < 0.0f ? q : 1.0f - q;
         a = z * p;
-        d = __fmaf_rn(z * RSQRT_2PI, expf(-0.5f * z * z), p);
+        d = __fmaf_rn(z * RSQRT_2PI, e, p);
     } else if constexpr (ACT == W4A8_ACT_GELU_TANH) {
-        const float z2 = z * z;
-        const Logistic l = logistic(2.0f * GELU_C * __fmaf_rn(GELU_A * z2, z, z));
+        const Logistic l = logistic2(gelu_tanh_arg(z));
         a = z * l.s;
-        d = __fmaf_rn(z * l.s * l.c, 2.0f * GELU_C * __fmaf_rn(3.0f * GELU_A, z2, 1.0f), l.s);
+        // (a l.c is 0 long before z^2 overflows; the cap keeps the product a number)
+        d = __fmaf_rn(a * l.c, 2.0f * GELU_C * __fmaf_rn(3.0f * GELU_A, fminf(z * z, 1e30f), 1.0f), l.s);
+    }
+}
+
+// The activation by its code: for places that finish few values.
+__device__ __noinline__ float act_any(int act, float z) {
+    switch (act) {
+        case W4A8_ACT_RELU: return act_value<W4A8_ACT_RELU>(z);
+        case W4A8_ACT_SILU: return act_value<W4A8_ACT_SILU>(z);
+        case W4A8_ACT_GELU: return act_value<W4A8_ACT_GELU>(z);
+        case W4A8_ACT_GELU_TANH: return act_value<W4A8_ACT_GELU_TANH>(z);
+        default: return z;
     }
 }
 

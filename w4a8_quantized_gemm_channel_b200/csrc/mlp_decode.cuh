@@ -238,7 +238,7 @@ k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
                     if constexpr (GLU) cb += sm.red[rb][w][8 + ch][tk];
                 }
                 const float rx = sm.rsx[tk];
-                const float z = dequant(ca, rx, ra, b0), u = GLU ? dequant(cb, rx, rc, b1) : 0.0f;
+                const float z = dequant(__int2float_rn(ca), rx, ra, b0), u = GLU ? dequant(__int2float_rn(cb), rx, rc, b1) : 0.0f;
                 float y = act_any(p.act, z);
                 if constexpr (GLU) y *= u;
                 else if (p.e.R) y += res[o];

@@ -333,14 +333,30 @@ __device__ __forceinline__ void load_tokens(float (&t)[16], const float *tok) {
     }
 }
 
+// INT32 accumulators (16 x the sum) to float. With `small`, |sum| < 2^22
+// (127 * 8 * K at most), the conversion is two additions: the sum's bits under
+// the exponent of 1.5 2^23, and that subtracted. The conversion instruction
+// shares the exponentials' slow pipe.
+constexpr int SMALL_K = (1 << 22) / (127 * 8);
+__device__ __forceinline__ void to_float(const uint32_t (&v)[16], bool small, float (&f)[16]) {
+    if (small) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            f[j] = (__uint_as_float(0x4B400000u + (uint32_t)((int32_t)v[j] >> 4)) - 12582912.0f);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = 0.0625f * __int2float_rn((int32_t)v[j]);
+    }
+}
+
 template <int ACT, bool GLU, bool SAVE, bool RES, typename T>
-__device__ __forceinline__ void fwd_unit(const uint32_t (&v)[16], const float (&r)[16], const float *tok, float rsw,
+__device__ __forceinline__ void fwd_unit(const float (&f)[16], const float (&r)[16], const float *tok, float rsw,
                                          float b, int lane, uint32_t st, int tile) {
     constexpr int ROW = (GLU ? 64 : 128) * (int)sizeof(T);
     float z[16];
     load_tokens(z, tok);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) z[j] = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[j]), z[j]), rsw) + b;
+    for (int j = 0; j < 16; ++j) z[j] = dequant(f[j], z[j], rsw, b);
     if constexpr (GLU) {
         // lanes 0-15 finish tokens 0-7 of the unit, lanes 16-31 tokens 8-15
         const bool gate = lane < 16;
@@ -371,7 +387,7 @@ __device__ __forceinline__ void fwd_unit(const uint32_t (&v)[16], const float (&
 }
 
 template <int ACT, bool GLU, typename T>
-__device__ __forceinline__ void fwd_unit_any(bool save, bool res, const uint32_t (&v)[16], const float (&r)[16],
+__device__ __forceinline__ void fwd_unit_any(bool save, bool res, const float (&v)[16], const float (&r)[16],
                                              const float *tok, float rsw, float b, int lane, uint32_t st, int tile) {
     if (GLU || !res) {
         if (save) fwd_unit<ACT, GLU, true, false, T>(v, r, tok, rsw, b, lane, st, tile);
@@ -386,12 +402,17 @@ __device__ __forceinline__ void fwd_unit_any(bool save, bool res, const uint32_t
 // alignment does not allow the TMA store.
 template <int COLS, typename T>
 __device__ __forceinline__ void copy_out(const uint8_t *stg, void *out, int ld, int m0, int M, int n0, int N, int et) {
-    const T *s = reinterpret_cast<const T *>(stg);
-    const int rows = min(UNIT, M - m0);
-    for (int i = et; i < rows * COLS; i += 128) {
-        const int r = i / COLS, c = i % COLS;
-        if (n0 + c < N) static_cast<T *>(out)[(size_t)(m0 + r) * ld + n0 + c] = s[i];
-    }
+    constexpr int STEP = 128 / COLS;  // rows per pass of the group
+    const T *s = reinterpret_cast<const T *>(stg) + et;
+    const int r0 = et / COLS, n = n0 + et % COLS;
+    if (n >= N) return;
+    T *o = static_cast<T *>(out) + (size_t)(m0 + r0) * ld + n;
+    T v[UNIT / STEP];
+#pragma unroll
+    for (int i = 0; i < UNIT / STEP; ++i) v[i] = s[128 * i];
+#pragma unroll
+    for (int i = 0; i < UNIT / STEP; ++i)
+        if (m0 + r0 + i * STEP < M) o[(size_t)(i * STEP) * ld] = v[i];
 }
 
 // Staging of a call: each group owns half of EPI_SMEM, as one set of tiles or
@@ -655,7 +676,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         const int col = GLU ? 16 * q + (lane & 15)
                             : FWD ? et : (et & ~7) | ((et & 7) >> 1) | ((et & 1) << 2);
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-        const bool res = FWD && !GLU && p.e.R != nullptr;
+        const bool res = FWD && !GLU && p.e.R != nullptr, small = p.depth <= SMALL_K;
         int buf = 0, set = 0;
         uint32_t acc_phase = 0;
         for (Run run = run0; run.valid(); run.next()) {
@@ -670,7 +691,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             if constexpr (FWD) {
                 const bool up = GLU && lane >= 16;
                 const float *sw = up ? p.b.sw : p.a.sw, *bias = up ? p.b.bias : p.a.bias;
-                rsw = n_ok ? __frcp_rn(ld_dep(sw + n)) * 0.0625f : 1.0f;  // the accumulator holds 16 x the sum
+                rsw = n_ok ? __frcp_rn(ld_dep(sw + n)) : 1.0f;
                 b = n_ok && bias ? ld_dep(bias + n) : 0.0f;
             }
             // One decision for all warps (this barrier also publishes the table).
@@ -704,7 +725,9 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(ptx::smem_addr(stg) + (uint32_t)(j * ROWS_CTA + et) * 4),
                                      "r"(v[j]));
                 } else if constexpr (FWD) {
-#define W4A8_UNIT(A) fwd_unit_any<A, GLU, T>(p.e.Z != nullptr, res, v, r, tok, rsw, b, lane, st, TILE)
+                    float f[16];
+                    to_float(v, small, f);
+#define W4A8_UNIT(A) fwd_unit_any<A, GLU, T>(p.e.Z != nullptr, res, f, r, tok, rsw, b, lane, st, TILE)
                     switch (p.act) {
                         case W4A8_ACT_NONE: W4A8_UNIT(W4A8_ACT_NONE); break;
                         case W4A8_ACT_RELU: W4A8_UNIT(W4A8_ACT_RELU); break;
@@ -854,7 +877,7 @@ k_mlp_join(const PairArgs p, int npairs) {
         const float t = ld_dep(p.tok + m);
         float y;
         if constexpr (FWD) {
-            const float z = __fmul_rn(__fmul_rn(__int2float_rn((int32_t)v[j]), __frcp_rn(t)), rsw) + bias;
+            const float z = dequant(__int2float_rn((int32_t)v[j]), __frcp_rn(t), rsw, bias);
             const float other = GLU ? __shfl_xor_sync(0xffffffffu, z, 16) : 0.0f;
             if (up || !n_ok) continue;
             y = act_any(p.act, z);

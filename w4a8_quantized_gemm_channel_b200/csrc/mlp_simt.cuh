@@ -21,10 +21,10 @@ struct EpiArgs {
     int ldr, ldy, ldz;
 };
 
-// z = acc / (sx sw) + b as (acc (1/sx)) (1/sw): two roundings beyond the
-// reciprocals', and no intermediate product of scales that could overflow.
-__device__ __forceinline__ float dequant(int32_t acc, float rsx, float rsw, float b) {
-    return __fmul_rn(__fmul_rn(__int2float_rn(acc), rsx), rsw) + b;
+// z = acc / (sx sw) + b as (acc (1/sx)) (1/sw) + b: no product of scales that
+// could overflow, the second product and the sum in one rounding.
+__device__ __forceinline__ float dequant(float acc, float rsx, float rsw, float b) {
+    return __fmaf_rn(__fmul_rn(acc, rsx), rsw, b);
 }
 
 // One thread per output. The row is in the k-permuted order, so a packed word
@@ -87,10 +87,10 @@ k_mlp_simt(const T *X, int ldx, int vec, const int8_t *Xq, int M, int K, int ldq
         }
         if (n >= N) continue;
         const float rx = __frcp_rn(s);
-        const float z = dequant(ca, rx, ra, ba);
+        const float z = dequant(__int2float_rn(ca), rx, ra, ba);
         float y = act_value<ACT>(z);
         if constexpr (GLU) {
-            const float u = dequant(cb, rx, rb, bb);
+            const float u = dequant(__int2float_rn(cb), rx, rb, bb);
             y *= u;
             if (e.U) st_elem(static_cast<T *>(e.U) + (size_t)m * e.ldz + n, u);
         } else {
