@@ -59,8 +59,10 @@ w4a8_status launch_quant_rows(const void *X, int M, int K, int ldx, const Worksp
     cudaError_t e;
     if (K <= 2048)
         e = launch_pdl(mlp::k_quant_rows<T, 128, 2>, grid, dim3(128), 0, s, x, M, K, ldx, ws.xq, ws.ldq, ws.sx, vec);
+    else if (K <= 4096)
+        e = launch_pdl(mlp::k_quant_rows<T, 256, 2>, grid, dim3(256), 0, s, x, M, K, ldx, ws.xq, ws.ldq, ws.sx, vec);
     else
-        e = launch_pdl(mlp::k_quant_rows<T, 512, 4>, grid, dim3(512), 0, s, x, M, K, ldx, ws.xq, ws.ldq, ws.sx, vec);
+        e = launch_pdl(mlp::k_quant_rows<T, 256, 6>, grid, dim3(256), 0, s, x, M, K, ldx, ws.xq, ws.ldq, ws.sx, vec);
     return from_cuda(e);
 }
 

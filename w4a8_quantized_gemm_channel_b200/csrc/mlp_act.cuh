@@ -72,14 +72,14 @@ __device__ __forceinline__ float act_value(float z) {
     return z;
 }
 
-// s(a) and 1 - s(a) of the logistic function at a with -a log2(e) given, from
-// exp(-|a|) in (0, 1]: no overflow, and no cancellation in 1 - s.
+// s(a) and 1 - s(a) of the logistic function, -a log2(e) given: e = exp(-a),
+// s = 1 / (1 + e), 1 - s = e s without cancellation, or 1 where s has become 0.
 struct Logistic {
     float s, c;
 };
 __device__ __forceinline__ Logistic logistic2(float minus_a_log2e) {
-    const float t = exp2_fast(-fabsf(minus_a_log2e)), r = rcp_fast(1.0f + t), q = t * r;
-    return minus_a_log2e <= 0.0f ? Logistic{r, q} : Logistic{q, r};
+    const float e = exp2_fast(minus_a_log2e), s = rcp_fast(1.0f + e);
+    return Logistic{s, s > 0.0f ? e * s : 1.0f};
 }
 
 // The activation and its derivative at z (ReLU's derivative at 0 is 0).
@@ -187,12 +187,51 @@ __device__ __forceinline__ uint2 row_codes8(const float (&v)[8], float s) {
     return make_uint2(__byte_perm(e0, e1, 0x5410), __byte_perm(o0, o1, 0x5410));
 }
 
+// Eight elements as loaded.
+template <typename T>
+struct Raw8 {
+    uint4 r[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *row, int i, int n, bool vec) {
+        if (vec && i + 8 <= n) {
+            r[0] = ld_dep_v4(row + i);
+            if constexpr (sizeof(T) == 4) r[1] = ld_dep_v4(row + i + 4);
+            return;
+        }
+        float v[8];
+        ld_row8(row, i, n, false, v);
+        if constexpr (sizeof(T) == 4) {
+            r[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            r[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+        } else {  // widened bfloat16: the upper halves
+            r[0] = make_uint4(__byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x7632),
+                              __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x7632),
+                              __byte_perm(__float_as_uint(v[4]), __float_as_uint(v[5]), 0x7632),
+                              __byte_perm(__float_as_uint(v[6]), __float_as_uint(v[7]), 0x7632));
+        }
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        if constexpr (sizeof(T) == 4) {
+            v[0] = __uint_as_float(r[0].x); v[1] = __uint_as_float(r[0].y);
+            v[2] = __uint_as_float(r[0].z); v[3] = __uint_as_float(r[0].w);
+            v[4] = __uint_as_float(r[1].x); v[5] = __uint_as_float(r[1].y);
+            v[6] = __uint_as_float(r[1].z); v[7] = __uint_as_float(r[1].w);
+        } else {
+            unpack_bf16x2(r[0].x, v[0], v[1]);
+            unpack_bf16x2(r[0].y, v[2], v[3]);
+            unpack_bf16x2(r[0].z, v[4], v[5]);
+            unpack_bf16x2(r[0].w, v[6], v[7]);
+        }
+    }
+};
+
 // Step 3 of the layer on rows of T: the arithmetic of k_act_quant (the same
 // scales and codes for the same float32 values; a bfloat16 is widened
 // exactly), codes stored in the k-permuted order of the nibble unpack (k0 k2
-// k4 k6 k1 k3 k5 k7 in every 8), the bytes from K to ldq zero. One block per
-// row; a row of up to THREADS x 8 x UNITS elements stays in registers between
-// the abs-max and the codes, a longer one is read twice. Bound: reading X.
+// k4 k6 k1 k3 k5 k7 in every 8), the bytes from K to ldq zero. Bound: reading X.
+//
+// One block per row, the row's bytes kept as loaded between the two steps (a
+// row that does not fit is read twice): few registers, so many blocks per SM
+// whose loads, reductions and stores overlap.
 template <typename T, int THREADS, int UNITS>
 __global__ void __launch_bounds__(THREADS)
 k_quant_rows(const T *X, int M, int K, int ldx, int8_t *__restrict__ Xq, int ldq, float *__restrict__ sx,
@@ -204,23 +243,29 @@ k_quant_rows(const T *X, int M, int K, int ldx, int8_t *__restrict__ Xq, int ldq
     griddep_launch_dependents();
     const int units = ldq / 8;
     const bool in_regs = units <= THREADS * UNITS;
+    auto peak = [](const Raw8<T> &r, float a) {
+        float v[8];
+        r.values(v);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) a = fmaxf(a, fabsf(v[b]));
+        return a;
+    };
     for (int m = blockIdx.x; m < M; m += gridDim.x) {
         const T *x = X + (size_t)m * ldx;
         uint2 *row = reinterpret_cast<uint2 *>(Xq + (size_t)m * ldq);
-        float v[UNITS][8], amax = 0.0f;
+        Raw8<T> raw[UNITS];
+        float amax = 0.0f;
         if (in_regs) {
 #pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-                ld_row8(x, 8 * ((int)threadIdx.x + i * THREADS), K, vec != 0, v[i]);
+            for (int i = 0; i < UNITS; ++i)
+                if ((int)threadIdx.x + i * THREADS < units) raw[i].load(x, 8 * ((int)threadIdx.x + i * THREADS), K, vec != 0);
 #pragma unroll
-                for (int b = 0; b < 8; ++b) amax = fmaxf(amax, fabsf(v[i][b]));
-            }
+            for (int i = 0; i < UNITS; ++i)
+                if ((int)threadIdx.x + i * THREADS < units) amax = peak(raw[i], amax);
         } else {
             for (int u = threadIdx.x; u < units; u += THREADS) {
-                float w[8];
-                ld_row8(x, 8 * u, K, vec != 0, w);
-#pragma unroll
-                for (int b = 0; b < 8; ++b) amax = fmaxf(amax, fabsf(w[b]));
+                raw[0].load(x, 8 * u, K, vec != 0);
+                amax = peak(raw[0], amax);
             }
         }
         const float s = act_scale_from_amax(block_max<THREADS>(amax, red));
@@ -229,13 +274,16 @@ k_quant_rows(const T *X, int M, int K, int ldx, int8_t *__restrict__ Xq, int ldq
 #pragma unroll
             for (int i = 0; i < UNITS; ++i) {
                 const int u = threadIdx.x + i * THREADS;
-                if (u < units) row[u] = row_codes8(v[i], s);
+                float v[8];
+                raw[i].values(v);
+                if (u < units) row[u] = row_codes8(v, s);
             }
         } else {
             for (int u = threadIdx.x; u < units; u += THREADS) {
-                float w[8];
-                ld_row8(x, 8 * u, K, vec != 0, w);
-                row[u] = row_codes8(w, s);
+                float v[8];
+                raw[0].load(x, 8 * u, K, vec != 0);
+                raw[0].values(v);
+                row[u] = row_codes8(v, s);
             }
         }
     }
@@ -304,16 +352,23 @@ k_grad_rows(GradIn<GLU, T> in, int M, int seg, __half *__restrict__ P, float *__
     griddep_launch_dependents();
     const int width = GLU ? 2 * seg : seg;
     // v of columns n..n+7: dz / sw
+    const bool swv = (reinterpret_cast<uintptr_t>(in.sw) & 15) == 0;
+    const bool suv = GLU && (reinterpret_cast<uintptr_t>(in.su) & 15) == 0;
     auto values = [&](int m, int n, float (&a)[8], float (&b)[8]) {
         in.template dz8<ACT>(m, n, a, b);
         float s[8];
-        ld_row8(in.sw, n, in.N, (reinterpret_cast<uintptr_t>(in.sw) & 15) == 0, s);
+        ld_row8(in.sw, n, in.N, swv, s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = n + i < in.N ? __fdividef(a[i], s[i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) a[i] *= rcp_fast(s[i]);
         if constexpr (GLU) {
-            ld_row8(in.su, n, in.N, (reinterpret_cast<uintptr_t>(in.su) & 15) == 0, s);
+            ld_row8(in.su, n, in.N, suv, s);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) b[i] = n + i < in.N ? __fdividef(b[i], s[i]) : 0.0f;
+            for (int i = 0; i < 8; ++i) b[i] *= rcp_fast(s[i]);
+        }
+        if (n + 8 > in.N) {  // past the row's end: 0 times the reciprocal of nothing
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (n + i >= in.N) a[i] = b[i] = 0.0f;
         }
     };
     auto keep = [&](int i, const float (&v)[8]) {
