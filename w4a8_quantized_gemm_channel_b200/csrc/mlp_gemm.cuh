@@ -73,17 +73,21 @@ struct Shape {
     static constexpr int A_BYTES = SUBS * SUB_BYTES;
     static constexpr int B_TILE = NT / 2 * 128;                 // one sub-tile or plane of the tokens
     static constexpr int B_BYTES = 2 * B_TILE;
-    // Slots per ring. 256 tokens leave shared memory for two widened stages.
-    static constexpr int A_SLOTS = NT == 256 && SUBS == 2 ? 2 : 3;
-    static constexpr int P_SLOTS = NT == 256 ? 2 : NT == 128 ? 3 : 4;
-    static constexpr int B_SLOTS = NT == 64 ? 4 : 3;
+    // Slots per ring: two widened stages with 256 tokens, three otherwise (two
+    // cost a fifth at 64 and 128 tokens), three of tokens, and as many of
+    // packed weights as fit: their loads come from HBM.
+    static constexpr int A_SLOTS = SUBS == 2 && NT == 256 ? 2 : 3;
+    static constexpr int B_SLOTS = 3;
+    static constexpr int REST = 232448 - 1024 - EPI_SMEM - 2048 - A_SLOTS * A_BYTES - B_SLOTS * B_BYTES;
+    static constexpr int P_SLOTS = REST / P_BYTES < 8 ? REST / P_BYTES : 8;
+    static_assert(P_SLOTS >= 2, "packed stages");
     // Widening: both groups on every stage (half each), which has a stage
     // ready soonest, or, where the MMAs of a stage are shorter than its
     // widening, the groups on every second stage, which hides the latencies of
     // one behind the other.
     static constexpr bool TURNS = NT < 256;
     static constexpr int WARPS_PER_STAGE = TURNS ? GROUP_WARPS : CONV_WARPS;
-    static_assert(B_SLOTS >= A_SLOTS, "A-slot reuse waits on a token slot's barrier");
+    static_assert(B_SLOTS >= A_SLOTS && P_SLOTS >= A_SLOTS, "A-slot reuse waits on a token slot's barrier");
 };
 
 template <int MODE, int NT>
@@ -105,6 +109,7 @@ struct alignas(1024) PairSmem {
     uint32_t tmem_base;
     int abort;
     int stop;                     // the epilogue gave up
+    uint32_t sink[CONV_WARPS];    // see give_back
 };
 
 struct PairArgs {
@@ -237,6 +242,17 @@ __device__ __forceinline__ void sts128(void *p, uint32_t a, uint32_t b, uint32_t
 template <int MODE>
 constexpr int pieces() { return MODE == BWD_TWO ? 1 : MODE == BWD_ONE ? 2 : 4; }
 
+// A load done exactly once: an ordinary one might be repeated at its use
+// instead of keeping the registers, after its slot has been given back.
+__device__ __forceinline__ uint4 lds128_once(const void *p) {
+    uint4 v;
+    asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(ptx::smem_addr(p))
+                 : "memory");
+    return v;
+}
+
 // WHOLE: the group takes the whole stage, its other half's pieces after its own.
 template <int MODE, bool WHOLE>
 __device__ __forceinline__ void load_pieces(uint4 (&v)[pieces<MODE>() * (WHOLE ? 2 : 1)], const uint8_t *packed, int g,
@@ -248,17 +264,33 @@ __device__ __forceinline__ void load_pieces(uint4 (&v)[pieces<MODE>() * (WHOLE ?
             const int r = tid, s = MODE == FWD_GLU ? ((r & 16) << 2) + ((r >> 5) << 4) + (r & 15) : r;
             const uint8_t *row = packed + half * (128 * 64) + s * 64;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[4 * h + c] = ptx::lds128(row + 16 * (c ^ ((s >> 1) & 3)));
+            for (int c = 0; c < 4; ++c) v[4 * h + c] = lds128_once(row + 16 * (c ^ ((s >> 1) & 3)));
         } else {
             const int n = tid & 63, c = tid >> 6;
             const uint8_t *row = packed + (MODE == BWD_ONE ? half * (64 * 64) : 0) + n * 64;
             if constexpr (MODE == BWD_ONE) {
-                v[2 * h] = ptx::lds128(row + 16 * (c ^ ((n >> 1) & 3)));
-                v[2 * h + 1] = ptx::lds128(row + 16 * ((c + 2) ^ ((n >> 1) & 3)));
+                v[2 * h] = lds128_once(row + 16 * (c ^ ((n >> 1) & 3)));
+                v[2 * h + 1] = lds128_once(row + 16 * ((c + 2) ^ ((n >> 1) & 3)));
             } else {
-                v[h] = ptx::lds128(row + 16 * ((2 * half + c) ^ ((n >> 1) & 3)));
+                v[h] = lds128_once(row + 16 * ((2 * half + c) ^ ((n >> 1) & 3)));
             }
         }
+    }
+}
+
+// Gives a packed slot back once this warp's loads of v have returned: lane 0
+// stores a value that depends on each of them before it arrives. (An mbarrier
+// arrive does not wait for loads in flight; behind loads that were merely
+// issued it let the slot be refilled under them.)
+template <int N>
+__device__ __forceinline__ void give_back(uint64_t *bar, uint32_t *sink, const uint4 (&v)[N], int lane) {
+    uint32_t d = v[0].x;
+#pragma unroll
+    for (int i = 1; i < N; ++i) d ^= v[i].x;
+    __syncwarp();
+    if (lane == 0) {
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(ptx::smem_addr(sink)), "r"(d) : "memory");
+        ptx::mbar_arrive(bar);
     }
 }
 
@@ -438,7 +470,7 @@ static_assert(Staging<FWD_LINEAR, float>::TILE * 2 * EPI_GROUPS <= EPI_SMEM &&
 
 // Where a partial tile's unit goes: slot, CTA of the pair, unit; rows of 128 lanes.
 template <int NT>
-__host__ __device__ inline size_t part_offset(int slot, int rank, int unit) {
+__host__ __device__ constexpr size_t part_offset(int slot, int rank, int unit) {
     return (((size_t)slot * 2 + rank) * (NT / UNIT) + unit) * (UNIT * ROWS_CTA);
 }
 
@@ -635,29 +667,25 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         uint32_t pphase = 0, bphase = 0;
         uint32_t ophase = it0 >= A_SLOTS ? 0 : 1;             // below 0 it has the parity before the first
         for (int it = it0; it < total; it += STRIDE) {
-            // The packed bytes come into registers before the wait for the A
-            // slot: what follows the MMAs' end is only the widening and its
-            // stores. (Their slot is given back after the stores, which need
-            // the values: given back right behind the loads it was refilled
-            // under them.)
+            // The packed bytes come into registers, and their slot is given
+            // back, before the wait for the A slot: what follows the MMAs' end
+            // is only the widening and its stores.
             // (A group that takes every second stage waits for the A slot first:
-            // the stage whose MMAs it then knows done had the same packed slot,
-            // so the parity of its own wait cannot be mistaken for the phase
-            // before, which the other group consumes.)
+            // all stages up to it - A_SLOTS are then done, among them the last
+            // ones in its packed and token slots, so the parity of its own waits
+            // cannot be mistaken for a phase that the other group consumes.)
             if (S::TURNS && it >= A_SLOTS && !warp_wait(&sm.empty[old], ophase, abort)) break;
             if (!warp_wait(&sm.pfull[ps], pphase, abort)) break;
             uint4 v[PIECES];
             load_pieces<MODE, S::TURNS>(v, sm.packed[ps], grp, tid);
+            give_back<PIECES>(&sm.pfree[ps], &sm.sink[warp - FIRST_CONV], v, lane);
             if (!warp_wait(&sm.bfull[bs], bphase, abort)) break;
             // the A slot was last read by the MMAs of iteration it - A_SLOTS
             if (!S::TURNS && it >= A_SLOTS && !warp_wait(&sm.empty[old], ophase, abort)) break;
             widen_pieces<MODE, S::TURNS>(v, sm.a[as], grp, tid);
             tcp::fence_proxy_async_smem();  // the slot's generic writes, before the MMA reads them
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(&sm.pfree[ps]);
-                tcp::mbar_arrive_leader(&sm.ready[as]);
-            }
+            if (lane == 0) tcp::mbar_arrive_leader(&sm.ready[as]);
             if ((ps += STRIDE) >= S::P_SLOTS) { ps -= S::P_SLOTS; pphase ^= 1u; }
             if ((bs += STRIDE) >= B_SLOTS) { bs -= B_SLOTS; bphase ^= 1u; }
             if ((old += STRIDE) >= B_SLOTS) { old -= B_SLOTS; ophase ^= 1u; }
@@ -824,9 +852,11 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
 
 // Finishes the tiles that k_mlp_pair left in parts. Block (b, unit): the tile
 // that holds the boundary between the runs of pairs b and b + 1, if b is the
-// first boundary inside it; one unit of 16 tokens; thread: a TMEM lane of one
-// of the pair's CTAs. Parts are added in the order of their stages, so results
+// first boundary inside it; JOIN tokens; thread: a TMEM lane of one of the
+// pair's CTAs. Parts are added in the order of their stages, so results
 // repeat bit for bit (INT32 sums are exact anyway).
+constexpr int JOIN = 4;
+static_assert(UNIT % JOIN == 0, "a block's tokens lie in one unit");
 template <int MODE, int NT, typename T>
 __global__ void __launch_bounds__(256)
 k_mlp_join(const PairArgs p, int npairs) {
@@ -837,28 +867,38 @@ k_mlp_join(const PairArgs p, int npairs) {
     const int tiles_m = (p.M + NT - 1) / NT, tiles_n = (p.N + TILE_ROWS - 1) / TILE_ROWS;
     const long long all = (long long)tiles_m * tiles_n * p.stages;
     auto bound = [&](int i) { return all * i / npairs; };  // where pair i's run begins
-    const int b = blockIdx.x, unit = blockIdx.y;
+    const int b = blockIdx.x, unit = blockIdx.y * JOIN / UNIT, j0 = blockIdx.y * JOIN % UNIT;
     const long long x = bound(b + 1);
     const int tile = (int)(x / p.stages);
     const long long t0 = (long long)tile * p.stages, t1 = t0 + p.stages;
     if (x == t0 || x >= all || bound(b) > t0) return;  // no tile inside, or an earlier boundary's
-    const int m0 = (tile % tiles_m) * NT + unit * UNIT;
+    const int m0 = (tile % tiles_m) * NT + unit * UNIT + j0;
     if (m0 >= p.M) return;
     const int rank = threadIdx.x >> 7, et = threadIdx.x & 127, lane = et & 31;
-    uint32_t v[16];
-    for (int q = b; q < npairs && bound(q) < t1; ++q) {
-        if (bound(q + 1) == bound(q)) continue;
-        // the tile is the first of q's run unless the run began in another tile
-        const int slot = 2 * q + (q == b && bound(q) < t0 ? 1 : 0);
-        const uint32_t *src = p.parts + part_offset<NT>(slot, rank, unit) + et;
+    // the parts: the tile is the first of its run except, perhaps, in run b
+    const int parts = (int)((t1 * npairs + all - 1) / all) - b;
+    const uint32_t *src = p.parts + part_offset<NT>(2 * b, rank, unit) + (size_t)j0 * ROWS_CTA + et;
+    constexpr size_t SLOT = part_offset<NT>(1, 0, 0);
+    uint32_t v[JOIN];
+    for (int q0 = 0; q0 < parts; q0 += 4) {  // four parts' loads in flight, added in order
+        uint32_t w[4][JOIN];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            uint32_t w;
-            asm volatile("ld.global.u32 %0, [%1];" : "=r"(w) : "l"(src + j * ROWS_CTA));
-            if (q == b) v[j] = w;
-            else if constexpr (FWD) v[j] += w;
-            else v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w));
-        }
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < JOIN; ++j)
+                if (q0 + q < parts) {
+                    const size_t slot = q0 + q == 0 ? (bound(b) < t0 ? 1 : 0) : 2 * (size_t)(q0 + q);
+                    asm volatile("ld.global.u32 %0, [%1];" : "=r"(w[q][j]) : "l"(src + slot * SLOT + j * ROWS_CTA));
+                }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < JOIN; ++j)
+                if (q0 + q < parts) {
+                    if (q0 + q == 0) v[j] = w[q][j];
+                    else if constexpr (FWD) v[j] += w[q][j];
+                    else v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[q][j]));
+                }
     }
     const int col = GLU ? 16 * (et >> 5) + (lane & 15) : FWD ? et : (et & ~7) | ((et & 7) >> 1) | ((et & 1) << 2);
     const int n = (tile / tiles_m) * TILE_ROWS + rank * COLS + col;
@@ -870,28 +910,51 @@ k_mlp_join(const PairArgs p, int npairs) {
         rsw = n_ok ? __frcp_rn(ld_dep(w.sw + n)) * 0.0625f : 1.0f;
         bias = n_ok && w.bias ? ld_dep(w.bias + n) : 0.0f;
     }
+    const int rows = min(JOIN, p.M - m0);
+    float t[JOIN], z[JOIN], u[JOIN];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const int m = m0 + j;
-        if (m >= p.M) break;
-        const float t = ld_dep(p.tok + m);
-        float y;
-        if constexpr (FWD) {
-            const float z = dequant(__int2float_rn((int32_t)v[j]), __frcp_rn(t), rsw, bias);
-            const float other = GLU ? __shfl_xor_sync(0xffffffffu, z, 16) : 0.0f;
-            if (up || !n_ok) continue;
-            y = act_any(p.act, z);
-            if constexpr (GLU) y *= other;
-            else if (p.e.R) y += ld_elem(static_cast<const T *>(p.e.R) + (size_t)m * p.e.ldr + n);
-            if (p.e.Z) {
-                st_elem(static_cast<T *>(p.e.Z) + (size_t)m * p.e.ldz + n, z);
-                if constexpr (GLU) st_elem(static_cast<T *>(p.e.U) + (size_t)m * p.e.ldz + n, other);
-            }
-        } else {
-            if (!n_ok) continue;
-            y = __uint_as_float(v[j]) * t;
+    for (int j = 0; j < JOIN; ++j) t[j] = ld_dep(p.tok + m0 + min(j, rows - 1));
+    if constexpr (FWD) {
+#pragma unroll
+        for (int j = 0; j < JOIN; ++j) {
+            z[j] = dequant(__int2float_rn((int32_t)v[j]), __frcp_rn(t[j]), rsw, bias);
+            u[j] = GLU ? __shfl_xor_sync(0xffffffffu, z[j], 16) : 0.0f;
         }
-        st_elem(static_cast<T *>(p.e.Y) + (size_t)m * p.e.ldy + n, y);
+        if (up || !n_ok) return;
+        if (!GLU && p.e.R) {
+            const T *R = static_cast<const T *>(p.e.R) + (size_t)m0 * p.e.ldr + n;
+#pragma unroll
+            for (int j = 0; j < JOIN; ++j) u[j] = j < rows ? ld_elem(R + (size_t)j * p.e.ldr) : 0.0f;
+        }
+        auto finish = [&](auto A) {
+            T *Y = static_cast<T *>(p.e.Y) + (size_t)m0 * p.e.ldy + n;
+#pragma unroll
+            for (int j = 0; j < JOIN; ++j) {
+                const float a = act_value<decltype(A)::value>(z[j]);
+                if (j < rows) st_elem(Y + (size_t)j * p.e.ldy, GLU ? a * u[j] : a + u[j]);
+            }
+        };
+        switch (p.act) {
+            case W4A8_ACT_NONE: finish(std::integral_constant<int, W4A8_ACT_NONE>{}); break;
+            case W4A8_ACT_RELU: finish(std::integral_constant<int, W4A8_ACT_RELU>{}); break;
+            case W4A8_ACT_SILU: finish(std::integral_constant<int, W4A8_ACT_SILU>{}); break;
+            case W4A8_ACT_GELU: finish(std::integral_constant<int, W4A8_ACT_GELU>{}); break;
+            default: finish(std::integral_constant<int, W4A8_ACT_GELU_TANH>{}); break;
+        }
+        if (p.e.Z) {
+#pragma unroll
+            for (int j = 0; j < JOIN; ++j) {
+                if (j >= rows) break;
+                st_elem(static_cast<T *>(p.e.Z) + (size_t)(m0 + j) * p.e.ldz + n, z[j]);
+                if constexpr (GLU) st_elem(static_cast<T *>(p.e.U) + (size_t)(m0 + j) * p.e.ldz + n, u[j]);
+            }
+        }
+    } else {
+        if (!n_ok) return;
+        T *Y = static_cast<T *>(p.e.Y) + (size_t)m0 * p.e.ldy + n;
+#pragma unroll
+        for (int j = 0; j < JOIN; ++j)
+            if (j < rows) st_elem(Y + (size_t)j * p.e.ldy, __uint_as_float(v[j]) * t[j]);
     }
 }
 
@@ -904,10 +967,12 @@ constexpr int PAIRS = 74;
 
 // Token tile and sharing of a call, by estimated time: rounds of whole tiles,
 // or equal runs of stages plus the join. Measured per stage of 8 MMAs: about
-// 760 ns with 256 tokens (1.0 us the two-plane forms' stage of the same
-// length is included), 480 with 128, 400 with 64; the last tile's epilogue
-// about 5 us per 256 tokens; the join about 3 us and the partial tiles' two
-// passes at 4 TB/s.
+// 760 ns with 256 tokens, 530 with 128, 500 with 64; the last tile's epilogue
+// about 5 us per 256 tokens; sharing costs the join's launch, the partial
+// tiles written and read (2 x 74 slots; 24 us with 256 tokens), and it is taken
+// only where the estimate gains a twentieth: with long sums the card's power
+// limit, not the idle pairs, sets the pace (2048 x 28672 x 4096: 210 us shared,
+// whole tiles 188).
 struct PairPlan {
     int nt;
     bool split;
@@ -917,7 +982,7 @@ inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages) {
     PairPlan best = {256, false, 0};
     double best_t = -1.0;
     const int cand[3] = {256, 128, 64};
-    const double stage_ns[3] = {760.0, 480.0, 400.0};
+    const double stage_ns[3] = {760.0, 530.0, 500.0};
     for (int i = 0; i < 3; ++i) {
         const int nt = cand[i];
         const long long tiles = (long long)((M + nt - 1) / nt) * ((rows + tile_rows - 1) / tile_rows);
@@ -927,8 +992,8 @@ inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages) {
             best = {nt, false, 0};
         }
         const size_t slot = (size_t)256 * nt * 4;
-        const double share = (double)((tiles * stages + PAIRS - 1) / PAIRS) * stage_ns[i] + 20.0 * nt + 3000.0 +
-                             2.0 * PAIRS * slot / 2000.0;
+        const double share = 1.05 * ((double)((tiles * stages + PAIRS - 1) / PAIRS) * stage_ns[i] + 20.0 * nt +
+                                     3000.0 + 24000.0 * nt / 256.0);
         if (tiles * stages >= PAIRS && share < best_t) {
             best_t = share;
             best = {nt, true, 2 * PAIRS * slot};
@@ -1003,7 +1068,7 @@ w4a8_status launch_pair(PairArgs p, const PairCall &c, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, wa, wb, x, out[0], out[1], out[2], p);
     if (e == cudaSuccess && p.parts)
-        e = launch_pdl(k_mlp_join<MODE, NT, T>, dim3(PAIRS - 1, (unsigned)((p.M < NT ? p.M : NT) + UNIT - 1) / UNIT),
+        e = launch_pdl(k_mlp_join<MODE, NT, T>, dim3(PAIRS - 1, (unsigned)((p.M < NT ? p.M : NT) + JOIN - 1) / JOIN),
                        dim3(256), 0, stream, p, PAIRS);
     return from_cuda(e);
 }
