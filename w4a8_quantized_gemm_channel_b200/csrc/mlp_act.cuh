@@ -432,7 +432,7 @@ k_grad_rows(GradIn<GLU, T> in, int M, int seg, __half *__restrict__ P, float *__
 // sums meet in shared memory in a fixed order, and a second kernel adds the
 // slices in order, so a run repeats bit for bit. Sums are float32 over at most
 // BG_ROWS / 8 rows, then 8, then the slices. Bound: HBM, the rows read once more.
-constexpr int BG_ROWS = 64;
+constexpr int BG_ROWS = 32;
 
 template <bool GLU, int ACT, typename T>
 __global__ void __launch_bounds__(256)

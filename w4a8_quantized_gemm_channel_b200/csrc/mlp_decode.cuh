@@ -60,7 +60,7 @@ template <int NTG>
 struct DecSmem {
     uint64_t full[DEC_RING], empty[DEC_RING];
     uint64_t rfull[DEC_RED], rfree[DEC_RED];
-    float part[dbulk::CONSUMER_WARPS];
+    float part[8][dbulk::CONSUMER_WARPS];
     float rsx[8 * NTG];
     int32_t red[DEC_RED][dbulk::CONSUMER_WARPS][16][8 * NTG + 1];
     int abort;
@@ -70,32 +70,46 @@ template <int NTG>
 constexpr int dec_static() { return ((int)sizeof(DecSmem<NTG>) + 1023) / 1024 * 1024 + 1024; }
 constexpr int DEC_SM_SMEM = 226 * 1024;  // what blocks may take of an SM's shared memory
 
-// Quantize row r of X (J units of 8 values per thread) into xs.
-template <int J, typename T>
-__device__ __forceinline__ void dec_quantize(const DecArgs &p, int r, int ks, int8_t *xs, float *part, float *rsx, int tid) {
-    float v[J][8], a = 0.0f;
-    const T *x = static_cast<const T *>(p.X) + (size_t)r * p.ldx;
+// Quantize the M <= R rows of X (J units of 8 values per thread and row) into
+// xs, all rows at once: one round of loads, one barrier for the abs-maxima.
+template <int R, int J, typename T>
+__device__ __forceinline__ void dec_quantize(const DecArgs &p, int ks, int pitch, int8_t *xs,
+                                             float (*part)[dbulk::CONSUMER_WARPS], float *rsx, int tid) {
+    Raw8<T> raw[R][J];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int k = 8 * (tid + DEC_CONSUMERS * j);
-        ld_row8(x, k, p.K, p.vec != 0, v[j]);
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int b = 0; b < 8; ++b) a = fmaxf(a, fabsf(v[j][b]));
+        for (int j = 0; j < J; ++j)  // rows past the last repeat it
+            raw[r][j].load(static_cast<const T *>(p.X) + (size_t)min(r, p.M - 1) * p.ldx,
+                           8 * (tid + DEC_CONSUMERS * j), p.K, p.vec != 0);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float a = 0.0f, v[8];
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            raw[r][j].values(v);
+#pragma unroll
+            for (int b = 0; b < 8; ++b) a = fmaxf(a, fabsf(v[b]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if ((tid & 31) == 0) part[r][tid >> 5] = a;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if ((tid & 31) == 0) part[tid >> 5] = a;
     ptx::bar_sync(1, DEC_CONSUMERS);
-    a = part[0];
 #pragma unroll
-    for (int w = 1; w < dbulk::CONSUMER_WARPS; ++w) a = fmaxf(a, part[w]);
-    ptx::bar_sync(1, DEC_CONSUMERS);  // part is rewritten by the next row
-    const float s = act_scale_from_amax(a);
-    if (tid == 0) rsx[r] = __frcp_rn(s);
+    for (int r = 0; r < R; ++r) {
+        if (r >= p.M) break;
+        float a = part[r][0], v[8];
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int k = 8 * (tid + DEC_CONSUMERS * j);
-        if (k < ks) *reinterpret_cast<uint2 *>(xs + k) = row_codes8(v[j], s);  // zeros past K
+        for (int w = 1; w < dbulk::CONSUMER_WARPS; ++w) a = fmaxf(a, part[r][w]);
+        const float s = act_scale_from_amax(a);
+        if (tid == 0) rsx[r] = __frcp_rn(s);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int k = 8 * (tid + DEC_CONSUMERS * j);
+            raw[r][j].values(v);
+            if (k < ks) *reinterpret_cast<uint2 *>(xs + (size_t)r * pitch + k) = row_codes8(v, s);  // zeros past K
+        }
     }
 }
 
@@ -131,8 +145,8 @@ __device__ __forceinline__ void dec_stage(int32_t (&acc)[NTG][2][4], const uint8
     }
 }
 
-// J > 0: FUSED with J units of 8 values per thread and row. J = 0: INT8 rows.
-template <bool GLU, int NTG, int J, typename T>
+// J > 0: FUSED, M <= R rows with J units of 8 values per thread and row. J = 0: INT8 rows.
+template <bool GLU, int NTG, int R, int J, typename T>
 __global__ void __launch_bounds__(DEC_THREADS, 2)
 k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const DecArgs p) {
     constexpr int TOK = 8 * NTG;
@@ -258,7 +272,7 @@ k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
     const int g = lane >> 2, t = lane & 3;
     griddep_wait();
     if constexpr (J > 0) {
-        for (int r = 0; r < p.M; ++r) dec_quantize<J, T>(p, r, ks, xs + (size_t)r * pitch, sm.part, sm.rsx, tid);
+        dec_quantize<R, J, T>(p, ks, pitch, xs, sm.part, sm.rsx, tid);
     } else {
         const int per = ks / 16, have = min(p.ldq, ks) / 16;
 #pragma unroll 4
@@ -302,6 +316,7 @@ k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 struct DecPlan {
     bool ok;
     int units;      // FUSED: units of 8 values per thread and row (1, 2, 4, 8), 0: INT8 rows
+    int rows;       // FUSED: M rounded up to a power of two
     int grid, ring, max_sb;
     size_t smem;
 };
@@ -337,15 +352,16 @@ inline DecPlan dec_plan(int M, int K, int N, int ch, int sms) {
             d.smem = (size_t)(ring * geo.stage_bytes() + xs);
             int j = 1;
             while (j * 8 * DEC_CONSUMERS < geo.pitch - 16) j *= 2;
-            d.units = j * M <= 8 ? j : 0;
+            d.rows = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8;
+            d.units = M <= 8 && j * d.rows <= 8 ? j : 0;
         }
     }
     return d;
 }
 
-template <bool GLU, int NTG, int J, typename T>
+template <bool GLU, int NTG, int R, int J, typename T>
 w4a8_status launch_decode(const DecPlan &d, DecArgs p, int ldp, cudaStream_t s) {
-    auto kern = k_mlp_decode<GLU, NTG, J, T>;
+    auto kern = k_mlp_decode<GLU, NTG, R, J, T>;
     constexpr int limit = 227 * 1024 - dec_static<NTG>();
     if (!raise_smem_limit(reinterpret_cast<const void *>(kern), limit)) return W4A8_ERR_CUDA;
     const DecGeo geo(p.K, d.max_sb);
@@ -362,12 +378,13 @@ w4a8_status launch_decode(const DecPlan &d, DecArgs p, int ldp, cudaStream_t s) 
 
 template <bool GLU, typename T>
 w4a8_status launch_decode_any(const DecPlan &d, const DecArgs &p, int ldp, cudaStream_t s) {
-    if (d.units == 1) return launch_decode<GLU, 1, 1, T>(d, p, ldp, s);
-    if (d.units == 2) return launch_decode<GLU, 1, 2, T>(d, p, ldp, s);
-    if (d.units == 4) return launch_decode<GLU, 1, 4, T>(d, p, ldp, s);
-    if (d.units == 8) return launch_decode<GLU, 1, 8, T>(d, p, ldp, s);
-    if (p.M <= 8) return launch_decode<GLU, 1, 0, T>(d, p, ldp, s);
-    return launch_decode<GLU, 2, 0, T>(d, p, ldp, s);
+#define W4A8_DEC(R, J) \
+    if (d.rows == R && d.units == J) return launch_decode<GLU, 1, R, J, T>(d, p, ldp, s);
+    W4A8_DEC(1, 1) W4A8_DEC(1, 2) W4A8_DEC(1, 4) W4A8_DEC(1, 8) W4A8_DEC(2, 1) W4A8_DEC(2, 2) W4A8_DEC(2, 4)
+    W4A8_DEC(4, 1) W4A8_DEC(4, 2) W4A8_DEC(8, 1)
+#undef W4A8_DEC
+    if (p.M <= 8) return launch_decode<GLU, 1, 1, 0, T>(d, p, ldp, s);
+    return launch_decode<GLU, 2, 1, 0, T>(d, p, ldp, s);
 }
 
 }  // namespace mlp
