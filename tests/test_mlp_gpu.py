@@ -364,3 +364,38 @@ def test_many_calls_give_the_same_bits(m, k, n, io):
         first = call()
         again = [call() for _ in range(200)]
         assert all(torch.equal(first, a) for a in again)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_gradients_of_very_wide_layers(io):
+    """Rows whose values exceed a block's shared memory."""
+    rnd, m, k = gen(21), 3, 40
+    for n, glu in ((56400, False), (28300, True)):
+        (qg, sg, wg), (qu, su, wu) = weights(rnd, n, k), weights(rnd, n, k)
+        dh, g, u = rnd(m, n, std=0.01).to(DT[io]), rnd(m, n).to(DT[io]), rnd(m, n).to(DT[io])
+        if glu:
+            got = native.w4a8_glu_grad(dh, g, u, wg, sg, wu, su, k)
+            want, _ = ref.glu_grad(dh, g, u, qg, sg, qu, su, "silu", True)
+        else:
+            got = native.w4a8_linear_act_grad(dh, wg, sg, k, act="silu", z=g)
+            want, _ = ref.linear_grad(dh, g, qg, sg, "silu", True)
+        ref.check(got, *want, f"N = {n}")
+
+
+def test_longest_sums():
+    """K at its limit (the largest INT32 sums) and rows longer than a block
+    holds, few rows and many."""
+    rnd, k, n = gen(22), native.ACT_MAX_K, 24
+    q, sw, wp = weights(rnd, n, k)
+    q[:2] = 7                       # codes and rows at their largest: |16 acc| just below 2^31
+    wp, x = ref.pack(q), None
+    for m in (1, 40):
+        x = rnd(m, k)
+        x[0] = 1.0
+        want = ref.linear(x, q, sw, None, "none", None)[0]
+        for path, got in paths_for(lambda p: native.w4a8_linear_act(x, wp, sw, path=p)):
+            ref.check(got, *want, f"m {m} {path}")
+    with pytest.raises(native.W4A8Error):
+        native.w4a8_linear_act(torch.zeros(1, k + 1, device="cuda"),
+                               torch.zeros(1, native.packed_ld(k + 1), dtype=torch.uint8, device="cuda"),
+                               torch.ones(1, device="cuda"))

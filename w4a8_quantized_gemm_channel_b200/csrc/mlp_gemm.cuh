@@ -967,9 +967,9 @@ constexpr int PAIRS = 74;
 
 // Token tile and sharing of a call, by estimated time: rounds of whole tiles,
 // or equal runs of stages plus the join. Measured per stage of 8 MMAs: about
-// 760 ns with 256 tokens, 530 with 128, 500 with 64; the last tile's epilogue
+// 760 ns with 256 tokens, 540 with 128, 600 with 64; the last tile's epilogue
 // about 5 us per 256 tokens; sharing costs the join's launch, the partial
-// tiles written and read (2 x 74 slots; 24 us with 256 tokens), and it is taken
+// tiles written and read (2 x 74 slots; some 16 us with 256 tokens), and it is taken
 // only where the estimate gains a twentieth: with long sums the card's power
 // limit, not the idle pairs, sets the pace (2048 x 28672 x 4096: 210 us shared,
 // whole tiles 188).
@@ -982,7 +982,7 @@ inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages) {
     PairPlan best = {256, false, 0};
     double best_t = -1.0;
     const int cand[3] = {256, 128, 64};
-    const double stage_ns[3] = {760.0, 530.0, 500.0};
+    const double stage_ns[3] = {760.0, 540.0, 600.0};
     for (int i = 0; i < 3; ++i) {
         const int nt = cand[i];
         const long long tiles = (long long)((M + nt - 1) / nt) * ((rows + tile_rows - 1) / tile_rows);
@@ -993,7 +993,7 @@ inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages) {
         }
         const size_t slot = (size_t)256 * nt * 4;
         const double share = 1.05 * ((double)((tiles * stages + PAIRS - 1) / PAIRS) * stage_ns[i] + 20.0 * nt +
-                                     3000.0 + 24000.0 * nt / 256.0);
+                                     3000.0 + 16000.0 * nt / 256.0);
         if (tiles * stages >= PAIRS && share < best_t) {
             best_t = share;
             best = {nt, true, 2 * PAIRS * slot};
