@@ -71,6 +71,12 @@ struct Shape {
     static constexpr int P_SUB = FWD ? 128 * 64 : 64 * 64;      // packed bytes per sub-tile
     static constexpr int P_BYTES = SUBS * P_SUB;
     static constexpr int A_BYTES = SUBS * SUB_BYTES;
+    // Float32 gradients: an accumulator takes this many stages (256 n) and the
+    // epilogue adds it to a sum in registers, rounded to nearest. The tensor
+    // core's own adder truncates, an error that grows with the length of the
+    // sum (1.4e-9 of the result per n: 1.8e-6 at 1001 n, against 0.5e-6 for
+    // rounded additions).
+    static constexpr int CHUNK = PLANES == 2 ? 4 : 1 << 30;
     static constexpr int B_TILE = NT / 2 * 128;                 // one sub-tile or plane of the tokens
     static constexpr int B_BYTES = 2 * B_TILE;
     // Slots per ring: two widened stages with 256 tokens, three otherwise (two
@@ -623,20 +629,22 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             uint32_t aphase = 0, bphase = 0;
             bool ok = true;
             for (Run r = run0; r.valid() && ok; r.next()) {
-                if (!warp_wait(&sm.acc_empty[buf], bphase ^ 1u, abort)) break;
-                const uint32_t d = tmem + (uint32_t)(buf * 256);
+                uint32_t d = 0;
                 int seg_st = r.s0 >= p.seg_stages ? r.s0 - p.seg_stages : r.s0;
                 int left = p.depth - S::STEP * seg_st;
                 for (int st = r.s0; st < r.s1; ++st) {
-                    ok = warp_wait(&sm.ready[as], aphase, abort);
+                    const bool fresh = (st - r.s0) % S::CHUNK == 0;  // a new accumulator
+                    ok = !fresh || warp_wait(&sm.acc_empty[buf], bphase ^ 1u, abort);
+                    ok = ok && warp_wait(&sm.ready[as], aphase, abort);
                     if (!ok) break;
+                    d = tmem + (uint32_t)(buf * 256);
                     ptx::tc_fence_after();
                     const uint64_t a = a0 + (uint32_t)(as * S::A_BYTES / 16), b = b0 + (uint32_t)(slot * S::B_BYTES / 16);
                     auto mma = [&](int i) {
                         const int sub = S::SUBS == 2 ? i >> 2 : 0, kk = i & 3;
                         const uint64_t ad = a + (uint32_t)((sub * SUB_BYTES + kk * A_STEP) / 16);
                         const uint64_t bd = b + (uint32_t)(((i >> 2) * S::B_TILE + 32 * kk) / 16);
-                        if (one) mma_ss2<FWD>(d, ad, bd, idesc, st != r.s0 || i != 0);
+                        if (one) mma_ss2<FWD>(d, ad, bd, idesc, !fresh || i != 0);
                     };
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mma(i);
@@ -649,9 +657,11 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                     if (++seg_st == p.seg_stages) { seg_st = 0; left = p.depth; }
                     if (++slot == B_SLOTS) slot = 0;
                     if (++as == A_SLOTS) { as = 0; aphase ^= 1u; }
+                    if (st + 1 == r.s1 || (st + 1 - r.s0) % S::CHUNK == 0) {
+                        if (one) tcp::mma_commit2_both(&sm.acc_full[buf]);
+                        if (++buf == 2) { buf = 0; bphase ^= 1u; }
+                    }
                 }
-                if (ok && one) tcp::mma_commit2_both(&sm.acc_full[buf]);
-                if (++buf == 2) { buf = 0; bphase ^= 1u; }
             }
             if (total > 0 && one) tcp::mma_commit2_both(&sm.done);
         }
@@ -722,30 +732,20 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                 rsw = n_ok ? __frcp_rn(ld_dep(sw + n)) : 1.0f;
                 b = n_ok && bias ? ld_dep(bias + n) : 0.0f;
             }
-            // One decision for all warps (this barrier also publishes the table).
-            if (!ptx::bar_and(BAR_EPI, 128 * EPI_GROUPS, ptx::mbar_wait(&sm.acc_full[buf], acc_phase, abort))) {
-                sm.stop = 1;  // let the store warp leave too
-                bar_arrive(BAR_STAGED + 2 * eg + set, 160);
-                break;
-            }
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int c0 = UNIT * eg; c0 < NT; c0 += UNIT * EPI_GROUPS) {
+            // A unit's values, from TMEM or summed, through its staging tiles.
+            auto finish = [&](int c0, const uint32_t (&v)[16]) {
                 const int m0 = m_base + c0;
-                if (m0 >= p.M) break;
+                if (m0 >= p.M) return;
                 // the set is free: the store warp has seen its last stores read
                 ptx::bar_sync(BAR_FREE + 2 * eg + set, 160);
                 uint8_t *stg = sg.at(sm.epi, eg, set);
                 const uint32_t st = ptx::smem_addr(stg) + (uint32_t)(col * (int)sizeof(T));
-                uint32_t v[16];
                 float r[16];
                 if (res && !partial) {  // indexes past the edges repeat the last row or column
                     const T *R = static_cast<const T *>(p.e.R) + min(n, p.N - 1);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) r[j] = ld_elem(R + (size_t)min(m0 + j, p.M - 1) * p.e.ldr);
                 }
-                ptx::tmem_ld_32x32b_x16(tmem + lane_base + (uint32_t)(buf * 256 + c0), v);
-                ptx::tmem_wait_ld();
                 const float *tok = sm.tok + c0;
                 if (partial) {
 #pragma unroll
@@ -781,11 +781,67 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                 }
                 bar_arrive(BAR_STAGED + 2 * eg + set, 160);
                 if (sg.sets == 2) set ^= 1;
+            };
+            auto load_unit = [&](int c0, uint32_t (&v)[16]) {
+                ptx::tmem_ld_32x32b_x16(tmem + lane_base + (uint32_t)(buf * 256 + c0), v);
+                ptx::tmem_wait_ld();
+            };
+            auto drained = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tcp::mbar_arrive_leader(&sm.acc_empty[buf]);
+                if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+            };
+            // One decision for all warps (the first time, this barrier also
+            // publishes the table).
+            auto acc_ready = [&]() {
+                const bool got = ptx::bar_and(BAR_EPI, 128 * EPI_GROUPS, ptx::mbar_wait(&sm.acc_full[buf], acc_phase, abort));
+                ptx::tc_fence_after();
+                return got;
+            };
+            bool alive = acc_ready();
+            if constexpr (S::PLANES == 2) {
+                constexpr int MINE = NT / (UNIT * EPI_GROUPS);  // this group's units
+                float sum[MINE][16];
+#pragma unroll
+                for (int i = 0; i < MINE; ++i)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[i][j] = 0.0f;
+                for (int st = run.s0; alive && st < run.s1; st += S::CHUNK) {
+                    if (st > run.s0) alive = acc_ready();
+                    if (!alive) break;
+#pragma unroll
+                    for (int i = 0; i < MINE; ++i) {
+                        uint32_t v[16];
+                        load_unit(UNIT * (eg + EPI_GROUPS * i), v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[i][j] += __uint_as_float(v[j]);
+                    }
+                    drained();
+                }
+                if (alive) {
+#pragma unroll
+                    for (int i = 0; i < MINE; ++i) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(sum[i][j]);
+                        finish(UNIT * (eg + EPI_GROUPS * i), v);
+                    }
+                }
+            } else if (alive) {
+#pragma unroll 1
+                for (int c0 = UNIT * eg; c0 < NT && m_base + c0 < p.M; c0 += UNIT * EPI_GROUPS) {
+                    uint32_t v[16];
+                    load_unit(c0, v);
+                    finish(c0, v);
+                }
+                drained();
             }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tcp::mbar_arrive_leader(&sm.acc_empty[buf]);
-            if (++buf == 2) { buf = 0; acc_phase ^= 1; }
+            if (!alive) {
+                sm.stop = 1;  // let the store warp leave too
+                bar_arrive(BAR_STAGED + 2 * eg + set, 160);
+                break;
+            }
             ptx::bar_sync(BAR_EPI, 128 * EPI_GROUPS);  // the table is rewritten next tile
         }
     } else if (warp == 3) {
@@ -978,12 +1034,12 @@ struct PairPlan {
     bool split;
     size_t part_bytes;
 };
-inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages) {
+inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages, bool two = false) {
     PairPlan best = {256, false, 0};
     double best_t = -1.0;
     const int cand[3] = {256, 128, 64};
     const double stage_ns[3] = {760.0, 540.0, 600.0};
-    for (int i = 0; i < 3; ++i) {
+    for (int i = two ? 1 : 0; i < 3; ++i) {  // two planes: the sums of 256 tokens do not fit the registers
         const int nt = cand[i];
         const long long tiles = (long long)((M + nt - 1) / nt) * ((rows + tile_rows - 1) / tile_rows);
         const double whole = (double)((tiles + PAIRS - 1) / PAIRS) * stages * stage_ns[i] + 20.0 * nt;
@@ -1004,7 +1060,7 @@ inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages) {
 // Stages of a call: forward 256 k, gradient 128 n (64 for two planes) per segment.
 inline PairPlan forward_plan(int M, int K, int N, bool glu) { return pair_plan(M, N, glu ? 128 : 256, (K + 255) / 256); }
 inline PairPlan grad_plan(int M, int K, int segs, int seg, bool two) {
-    return pair_plan(M, K, 256, segs * (seg / (two ? 64 : 128)));
+    return pair_plan(M, K, 256, segs * (seg / (two ? 64 : 128)), two);
 }
 
 // What a launch needs beside PairArgs: the operands' shapes.
@@ -1076,7 +1132,8 @@ w4a8_status launch_pair(PairArgs p, const PairCall &c, cudaStream_t stream) {
 template <int MODE, typename T>
 w4a8_status launch_pair_any(const PairPlan &plan, PairArgs p, const PairCall &c, void *parts, cudaStream_t s) {
     p.parts = plan.split ? static_cast<uint32_t *>(parts) : nullptr;
-    if (plan.nt == 256) return launch_pair<MODE, 256, T>(p, c, s);
+    if constexpr (MODE != BWD_TWO)
+        if (plan.nt == 256) return launch_pair<MODE, 256, T>(p, c, s);
     if (plan.nt == 128) return launch_pair<MODE, 128, T>(p, c, s);
     return launch_pair<MODE, 64, T>(p, c, s);
 }
