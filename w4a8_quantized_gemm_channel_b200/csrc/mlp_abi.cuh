@@ -112,7 +112,10 @@ w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a
         const mlp::PairPlan plan = mlp::forward_plan(M, K, N, GLU);
         const mlp::PairArgs p = {M, N, K, stages, stages, ws.sx, a, b, ea, act, 0, 1, nullptr};
         const mlp::PairCall c = {a.Wp, b.Wp, N, ldp, ws.xq, M, ws.ldq};
-        st = mlp::launch_pair_any<GLU ? mlp::FWD_GLU : mlp::FWD_LINEAR, T>(plan, p, c, ws_parts(ws, M), s);
+        st = by_act(act, [&](auto A) {
+            return mlp::launch_pair_any<GLU ? mlp::FWD_GLU : mlp::FWD_LINEAR, decltype(A)::value, T>(
+                plan, p, c, ws_parts(ws, M), s);
+        });
         if (st != W4A8_OK) return st;
         t_last_path = W4A8_PATH_TC;
         t_last_launches = plan.split ? 3 : 2;
@@ -219,7 +222,7 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
         const mlp::PairArgs p = {M, K, N, seg_stages, SEGS * seg_stages, ws.rs, {}, {},
                                  {nullptr, dX, nullptr, nullptr, 0, lddx, 0}, 0, 0, 1, nullptr};
         const mlp::PairCall c = {Wa, Wb, N, ldp, ws.P, ws.planes * M, SEGS * ws.seg};
-        st = mlp::launch_pair_any<LO ? mlp::BWD_TWO : mlp::BWD_ONE, T>(ws.plan, p, c, ws.tiles, s);
+        st = mlp::launch_pair_any<LO ? mlp::BWD_TWO : mlp::BWD_ONE, W4A8_ACT_NONE, T>(ws.plan, p, c, ws.tiles, s);
         if (st != W4A8_OK) return st;
         t_last_path = W4A8_PATH_TC;
         t_last_launches = launches + (ws.plan.split ? 3 : 2);

@@ -371,30 +371,14 @@ __device__ __forceinline__ void load_tokens(float (&t)[16], const float *tok) {
     }
 }
 
-// INT32 accumulators (16 x the sum) to float. With `small`, |sum| < 2^22
-// (127 * 8 * K at most), the conversion is two additions: the sum's bits under
-// the exponent of 1.5 2^23, and that subtracted. The conversion instruction
-// shares the exponentials' slow pipe.
-constexpr int SMALL_K = (1 << 22) / (127 * 8);
-__device__ __forceinline__ void to_float(const uint32_t (&v)[16], bool small, float (&f)[16]) {
-    if (small) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            f[j] = (__uint_as_float(0x4B400000u + (uint32_t)((int32_t)v[j] >> 4)) - 12582912.0f);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = 0.0625f * __int2float_rn((int32_t)v[j]);
-    }
-}
-
 template <int ACT, bool GLU, bool SAVE, bool RES, typename T>
-__device__ __forceinline__ void fwd_unit(const float (&f)[16], const float (&r)[16], const float *tok, float rsw,
+__device__ __forceinline__ void fwd_unit(const uint32_t (&v)[16], const float (&r)[16], const float *tok, float rsw,
                                          float b, int lane, uint32_t st, int tile) {
     constexpr int ROW = (GLU ? 64 : 128) * (int)sizeof(T);
     float z[16];
     load_tokens(z, tok);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) z[j] = dequant(f[j], z[j], rsw, b);
+    for (int j = 0; j < 16; ++j) z[j] = dequant(__int2float_rn((int32_t)v[j]), z[j], rsw, b);
     if constexpr (GLU) {
         // lanes 0-15 finish tokens 0-7 of the unit, lanes 16-31 tokens 8-15
         const bool gate = lane < 16;
@@ -425,7 +409,7 @@ __device__ __forceinline__ void fwd_unit(const float (&f)[16], const float (&r)[
 }
 
 template <int ACT, bool GLU, typename T>
-__device__ __forceinline__ void fwd_unit_any(bool save, bool res, const float (&v)[16], const float (&r)[16],
+__device__ __forceinline__ void fwd_unit_any(bool save, bool res, const uint32_t (&v)[16], const float (&r)[16],
                                              const float *tok, float rsw, float b, int lane, uint32_t st, int tile) {
     if (GLU || !res) {
         if (save) fwd_unit<ACT, GLU, true, false, T>(v, r, tok, rsw, b, lane, st, tile);
@@ -480,7 +464,10 @@ __host__ __device__ constexpr size_t part_offset(int slot, int rank, int unit) {
     return (((size_t)slot * 2 + rank) * (NT / UNIT) + unit) * (UNIT * ROWS_CTA);
 }
 
-template <int MODE, int NT, typename T>
+// ACT is a template argument of the kernel (none for the gradient): one kernel
+// with all activations behind a switch ran the epilogue-bound shapes 13 to 18 %
+// slower (M 4096, K 256).
+template <int MODE, int NT, int ACT, typename T>
 __global__ void __launch_bounds__(PAIR_THREADS, 1)
 k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CUtensorMap tm_wb,
            const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
@@ -714,7 +701,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
         const int col = GLU ? 16 * q + (lane & 15)
                             : FWD ? et : (et & ~7) | ((et & 7) >> 1) | ((et & 1) << 2);
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-        const bool res = FWD && !GLU && p.e.R != nullptr, small = p.depth <= SMALL_K;
+        const bool res = FWD && !GLU && p.e.R != nullptr;
         int buf = 0, set = 0;
         uint32_t acc_phase = 0;
         for (Run run = run0; run.valid(); run.next()) {
@@ -729,7 +716,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             if constexpr (FWD) {
                 const bool up = GLU && lane >= 16;
                 const float *sw = up ? p.b.sw : p.a.sw, *bias = up ? p.b.bias : p.a.bias;
-                rsw = n_ok ? __frcp_rn(ld_dep(sw + n)) : 1.0f;
+                rsw = n_ok ? __frcp_rn(ld_dep(sw + n)) * 0.0625f : 1.0f;  // the accumulator holds 16 x the sum
                 b = n_ok && bias ? ld_dep(bias + n) : 0.0f;
             }
             // A unit's values, from TMEM or summed, through its staging tiles.
@@ -753,17 +740,7 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                         asm volatile("st.shared.u32 [%0], %1;" ::"r"(ptx::smem_addr(stg) + (uint32_t)(j * ROWS_CTA + et) * 4),
                                      "r"(v[j]));
                 } else if constexpr (FWD) {
-                    float f[16];
-                    to_float(v, small, f);
-#define W4A8_UNIT(A) fwd_unit_any<A, GLU, T>(p.e.Z != nullptr, res, f, r, tok, rsw, b, lane, st, TILE)
-                    switch (p.act) {
-                        case W4A8_ACT_NONE: W4A8_UNIT(W4A8_ACT_NONE); break;
-                        case W4A8_ACT_RELU: W4A8_UNIT(W4A8_ACT_RELU); break;
-                        case W4A8_ACT_SILU: W4A8_UNIT(W4A8_ACT_SILU); break;
-                        case W4A8_ACT_GELU: W4A8_UNIT(W4A8_ACT_GELU); break;
-                        default: W4A8_UNIT(W4A8_ACT_GELU_TANH); break;
-                    }
-#undef W4A8_UNIT
+fwd_unit_any<ACT, GLU, T>(p.e.Z != nullptr, res, v, r, tok, rsw, b, lane, st, TILE);
                 } else {
                     float y[16];
                     load_tokens(y, tok);
@@ -1071,12 +1048,12 @@ struct PairCall {
     int x_rows, x_inner;         // rows and row elements (= stride) of X
 };
 
-template <int MODE, int NT, typename T>
+template <int MODE, int NT, int ACT, typename T>
 w4a8_status launch_pair(PairArgs p, const PairCall &c, cudaStream_t stream) {
     using S = Shape<MODE, NT>;
     constexpr bool GLU = MODE == FWD_GLU;
     constexpr int COLS = GLU ? 64 : 128, TILE_ROWS = 2 * COLS;
-    auto kern = k_mlp_pair<MODE, NT, T>;
+    auto kern = k_mlp_pair<MODE, NT, ACT, T>;
     const int smem = (int)sizeof(PairSmem<MODE, NT>) + 1024;
     if (!raise_smem_limit(reinterpret_cast<const void *>(kern), smem)) return W4A8_ERR_CUDA;
     CUtensorMap wa, wb, x, out[3];
@@ -1129,13 +1106,13 @@ w4a8_status launch_pair(PairArgs p, const PairCall &c, cudaStream_t stream) {
     return from_cuda(e);
 }
 
-template <int MODE, typename T>
+template <int MODE, int ACT, typename T>
 w4a8_status launch_pair_any(const PairPlan &plan, PairArgs p, const PairCall &c, void *parts, cudaStream_t s) {
     p.parts = plan.split ? static_cast<uint32_t *>(parts) : nullptr;
     if constexpr (MODE != BWD_TWO)
-        if (plan.nt == 256) return launch_pair<MODE, 256, T>(p, c, s);
-    if (plan.nt == 128) return launch_pair<MODE, 128, T>(p, c, s);
-    return launch_pair<MODE, 64, T>(p, c, s);
+        if (plan.nt == 256) return launch_pair<MODE, 256, ACT, T>(p, c, s);
+    if (plan.nt == 128) return launch_pair<MODE, 128, ACT, T>(p, c, s);
+    return launch_pair<MODE, 64, ACT, T>(p, c, s);
 }
 
 }  // namespace mlp
