@@ -198,14 +198,16 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
         constexpr int ACT = decltype(A)::value;
         if (dba || dbb) {
             const int slices = (M + mlp::BG_ROWS - 1) / mlp::BG_ROWS;
-            cudaError_t e = launch_pdl(mlp::k_bias_grad_part<GLU, ACT, T>,
-                                       dim3((N + 255) / 256, slices < 65535 ? slices : 65535), dim3(256), 0, s, in, M,
-                                       ws.part);
+            cudaError_t e = launch_pdl(mlp::k_bias_grad<GLU, ACT, T>,
+                                       dim3((N + mlp::BG_COLS - 1) / mlp::BG_COLS, slices < 65535 ? slices : 65535),
+                                       dim3(512), 0, s, in, M, ws.part, dba, dbb);
+            ++launches;
+            if (e == cudaSuccess && slices > 1) {
+                e = launch_pdl(mlp::k_bias_grad_sum, dim3((N + 255) / 256, SEGS), dim3(256), 0, s,
+                               (const float *)ws.part, slices, SEGS, N, dba, dbb);
+                ++launches;
+            }
             if (e != cudaSuccess) return (w4a8_status)W4A8_ERR_CUDA;
-            e = launch_pdl(mlp::k_bias_grad_sum, dim3((N + 255) / 256, SEGS), dim3(256), 0, s,
-                           (const float *)ws.part, slices, SEGS, N, dba, dbb);
-            if (e != cudaSuccess) return (w4a8_status)W4A8_ERR_CUDA;
-            launches += 2;
         }
         const int bytes = SEGS * ws.seg * (int)sizeof(float);
         const bool held = bytes <= mlp::GR_HELD_MAX;

@@ -427,28 +427,31 @@ k_grad_rows(GradIn<GLU, T> in, int M, int seg, __half *__restrict__ P, float *__
     }
 }
 
-// Bias gradients: column sums of dz. Block (256 columns, row slice): each of 8
-// warps adds every eighth row of the slice, eight columns per lane, the warps'
-// sums meet in shared memory in a fixed order, and a second kernel adds the
-// slices in order, so a run repeats bit for bit. Sums are float32 over at most
-// BG_ROWS / 8 rows, then 8, then the slices. Bound: HBM, the rows read once more.
-constexpr int BG_ROWS = 32;
+// Bias gradients: column sums of dz. Block (64 columns, slice of BG_ROWS rows):
+// 64 row groups of 8 lanes x 8 columns each take every 64th row of the slice,
+// their sums are added in a fixed order, so a run repeats bit for bit. One
+// slice writes the result; more leave partial sums that k_bias_grad_sum adds
+// in order. Sums are float32 over at most BG_ROWS / 64 rows, then 64, then the
+// slices. Bound: HBM, the rows read once more; at few rows the launch, hence
+// one where one slice covers them.
+constexpr int BG_ROWS = 256, BG_COLS = 64, BG_GROUPS = 64;
 
 template <bool GLU, int ACT, typename T>
-__global__ void __launch_bounds__(256)
-k_bias_grad_part(GradIn<GLU, T> in, int M, float *__restrict__ part) {
+__global__ void __launch_bounds__(512)
+k_bias_grad(GradIn<GLU, T> in, int M, float *part, float *dba, float *dbb) {
     constexpr int SEGS = GLU ? 2 : 1;
-    __shared__ float red[SEGS][8][256];
+    __shared__ float red[SEGS][BG_GROUPS][BG_COLS + 1];
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int n0 = blockIdx.x * 256, n = n0 + 8 * lane;
-    for (int slice = blockIdx.y; slice * BG_ROWS < M; slice += gridDim.y) {
+    const int c = threadIdx.x & 7, g = threadIdx.x >> 3;
+    const int n0 = blockIdx.x * BG_COLS, n = n0 + 8 * c;
+    const int slices = (M + BG_ROWS - 1) / BG_ROWS;
+    for (int slice = blockIdx.y; slice < slices; slice += gridDim.y) {
         const int m1 = min(M, (slice + 1) * BG_ROWS);
         float sa[8] = {}, sb[8] = {};
         if (n < in.N) {
-#pragma unroll 2
-            for (int m = slice * BG_ROWS + warp; m < m1; m += 8) {
+#pragma unroll 4
+            for (int m = slice * BG_ROWS + g; m < m1; m += BG_GROUPS) {
                 float a[8], b[8];
                 in.template dz8<ACT>(m, n, a, b);
 #pragma unroll
@@ -460,16 +463,18 @@ k_bias_grad_part(GradIn<GLU, T> in, int M, float *__restrict__ part) {
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            red[0][warp][8 * lane + i] = sa[i];
-            if constexpr (GLU) red[1][warp][8 * lane + i] = sb[i];
+            red[0][g][8 * c + i] = sa[i];
+            if constexpr (GLU) red[1][g][8 * c + i] = sb[i];
         }
         __syncthreads();
-        for (int s = 0; s < SEGS; ++s) {
-            const int c = threadIdx.x;
+        const int col = threadIdx.x % BG_COLS, s = threadIdx.x / BG_COLS;
+        if (s < SEGS && n0 + col < in.N) {
             float t = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) t += red[s][w][c];
-            if (n0 + c < in.N) part[((size_t)slice * SEGS + s) * in.N + n0 + c] = t;
+#pragma unroll 16
+            for (int w = 0; w < BG_GROUPS; ++w) t += red[s][w][col];
+            float *out = s == 0 ? dba : dbb;
+            if (slices > 1) part[((size_t)slice * SEGS + s) * in.N + n0 + col] = t;
+            else if (out != nullptr) out[n0 + col] = t;
         }
         __syncthreads();
     }

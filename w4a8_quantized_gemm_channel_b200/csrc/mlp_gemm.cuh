@@ -1003,7 +1003,7 @@ constexpr int PAIRS = 74;
 // 760 ns with 256 tokens, 540 with 128, 600 with 64; the last tile's epilogue
 // about 5 us per 256 tokens; sharing costs the join's launch, the partial
 // tiles written and read (2 x 74 slots; some 16 us with 256 tokens), and it is taken
-// only where the estimate gains a twentieth: with long sums the card's power
+// only where the estimate gains a tenth: with long sums the card's power
 // limit, not the idle pairs, sets the pace (2048 x 28672 x 4096: 210 us shared,
 // whole tiles 188).
 struct PairPlan {
@@ -1025,7 +1025,7 @@ inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages, bool two =
             best = {nt, false, 0};
         }
         const size_t slot = (size_t)256 * nt * 4;
-        const double share = 1.05 * ((double)((tiles * stages + PAIRS - 1) / PAIRS) * stage_ns[i] + 20.0 * nt +
+        const double share = 1.1 * ((double)((tiles * stages + PAIRS - 1) / PAIRS) * stage_ns[i] + 20.0 * nt +
                                      3000.0 + 16000.0 * nt / 256.0);
         if (tiles * stages >= PAIRS && share < best_t) {
             best_t = share;
