@@ -79,13 +79,24 @@ struct Shape {
     static constexpr int CHUNK = PLANES == 2 ? 4 : 1 << 30;
     static constexpr int B_TILE = NT / 2 * 128;                 // one sub-tile or plane of the tokens
     static constexpr int B_BYTES = 2 * B_TILE;
-    // Slots per ring: two widened stages with 256 tokens, three otherwise (two
-    // cost a fifth at 64 and 128 tokens), three of tokens, and as many of
-    // packed weights as fit: their loads come from HBM.
-    static constexpr int A_SLOTS = SUBS == 2 && NT == 256 ? 2 : 3;
-    static constexpr int B_SLOTS = 3;
-    static constexpr int REST = 232448 - 1024 - EPI_SMEM - 2048 - A_SLOTS * A_BYTES - B_SLOTS * B_BYTES;
+    // Where the widened weights go. With few tokens the MMAs of a stage read as
+    // much of A as with many, and A's way through shared memory (written and
+    // read, 64 KB a stage) is most of its traffic and sets the pace: 600 ns a
+    // stage with 64 tokens. The accumulators then leave TMEM free, so the
+    // forward forms of 128 and 64 tokens keep A there (tcgen05.st, no shared
+    // memory). The gradient's A is MN-major, which only shared memory can hold.
+    static constexpr bool A_TMEM = FWD && NT < 256;
+    static constexpr int A_COLS = STEP / 4;                     // TMEM columns of a stage of A
+    static constexpr int D_COLS = A_TMEM ? NT : 256;            // columns per accumulator
+    // Slots per ring: widened stages, tokens, and as many of packed weights as
+    // fit, up to eight: their loads come from HBM. (Two widened stages instead
+    // of three cost the gradient a fifth at 64 and 128 tokens.)
+    static constexpr int A_SLOTS = A_TMEM ? 4 : SUBS == 2 && NT == 256 ? 2 : 3;
+    static constexpr int B_SLOTS = A_TMEM ? 4 : 3;
+    static constexpr int A_SMEM = A_TMEM ? 0 : A_SLOTS * A_BYTES;
+    static constexpr int REST = 232448 - 1024 - EPI_SMEM - 2048 - A_SMEM - B_SLOTS * B_BYTES - (A_TMEM ? 1024 : 0);
     static constexpr int P_SLOTS = REST / P_BYTES < 8 ? REST / P_BYTES : 8;
+    static_assert(!A_TMEM || 2 * NT + A_SLOTS * A_COLS <= 512, "TMEM budget");
     static_assert(P_SLOTS >= 2, "packed stages");
     // Widening: both groups on every stage (half each), which has a stage
     // ready soonest, or, where the MMAs of a stage are shorter than its
@@ -100,7 +111,7 @@ template <int MODE, int NT>
 struct alignas(1024) PairSmem {
     using S = Shape<MODE, NT>;
     uint8_t b[S::B_SLOTS][S::B_BYTES];
-    uint8_t a[S::A_SLOTS][S::A_BYTES];
+    uint8_t a[S::A_TMEM ? 1 : S::A_SLOTS][S::A_TMEM ? 1024 : S::A_BYTES];
     uint8_t packed[S::P_SLOTS][S::P_BYTES];
     uint8_t epi[EPI_SMEM];
     uint64_t pfull[S::P_SLOTS];   // packed weights landed
@@ -340,6 +351,28 @@ __device__ __forceinline__ void widen_pieces(const uint4 (&v)[pieces<MODE>() * (
             widen_chunk(v[h], slot, tid & 63, 2 * half + (tid >> 6));
         }
     }
+}
+
+// A whole forward stage of row r to TMEM lane r (the thread's), 4 INT8 a column.
+__device__ __forceinline__ void widen_tmem(const uint4 (&v)[8], uint32_t taddr) {
+    constexpr uint32_t H = 0xF0F0F0F0u;
+    ptx::tc_fence_after();  // behind the wait for the MMAs that read the slot
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t o[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t p[4] = {v[4 * h + c].x, v[4 * h + c].y, v[4 * h + c].z, v[4 * h + c].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                o[8 * c + 2 * j] = (p[j] << 4) & H;
+                o[8 * c + 2 * j + 1] = p[j] & H;
+            }
+        }
+        ptx::tmem_st_32x32b_x32(taddr + 32 * h, o);
+    }
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
 }
 
 // ---------------------------------------------------------------- epilogue ---
@@ -624,14 +657,19 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
                     ok = !fresh || warp_wait(&sm.acc_empty[buf], bphase ^ 1u, abort);
                     ok = ok && warp_wait(&sm.ready[as], aphase, abort);
                     if (!ok) break;
-                    d = tmem + (uint32_t)(buf * 256);
+                    d = tmem + (uint32_t)(buf * S::D_COLS);
+                    const uint32_t ta = tmem + (uint32_t)(2 * NT + as * S::A_COLS);
                     ptx::tc_fence_after();
                     const uint64_t a = a0 + (uint32_t)(as * S::A_BYTES / 16), b = b0 + (uint32_t)(slot * S::B_BYTES / 16);
                     auto mma = [&](int i) {
                         const int sub = S::SUBS == 2 ? i >> 2 : 0, kk = i & 3;
                         const uint64_t ad = a + (uint32_t)((sub * SUB_BYTES + kk * A_STEP) / 16);
                         const uint64_t bd = b + (uint32_t)(((i >> 2) * S::B_TILE + 32 * kk) / 16);
-                        if (one) mma_ss2<FWD>(d, ad, bd, idesc, !fresh || i != 0);
+                        if constexpr (S::A_TMEM) {
+                            if (one) tcp::mma_i8_ts2(d, ta + 8 * i, bd, idesc, !fresh || i != 0);
+                        } else {
+                            if (one) mma_ss2<FWD>(d, ad, bd, idesc, !fresh || i != 0);
+                        }
                     };
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mma(i);
@@ -679,8 +717,12 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             if (!warp_wait(&sm.bfull[bs], bphase, abort)) break;
             // the A slot was last read by the MMAs of iteration it - A_SLOTS
             if (!S::TURNS && it >= A_SLOTS && !warp_wait(&sm.empty[old], ophase, abort)) break;
-            widen_pieces<MODE, S::TURNS>(v, sm.a[as], grp, tid);
-            tcp::fence_proxy_async_smem();  // the slot's generic writes, before the MMA reads them
+            if constexpr (S::A_TMEM) {
+                widen_tmem(v, tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(2 * NT + as * S::A_COLS));
+            } else {
+                widen_pieces<MODE, S::TURNS>(v, sm.a[as], grp, tid);
+                tcp::fence_proxy_async_smem();  // the slot's generic writes, before the MMA reads them
+            }
             __syncwarp();
             if (lane == 0) tcp::mbar_arrive_leader(&sm.ready[as]);
             if ((ps += STRIDE) >= S::P_SLOTS) { ps -= S::P_SLOTS; pphase ^= 1u; }
@@ -760,7 +802,7 @@ fwd_unit_any<ACT, GLU, T>(p.e.Z != nullptr, res, v, r, tok, rsw, b, lane, st, TI
                 if (sg.sets == 2) set ^= 1;
             };
             auto load_unit = [&](int c0, uint32_t (&v)[16]) {
-                ptx::tmem_ld_32x32b_x16(tmem + lane_base + (uint32_t)(buf * 256 + c0), v);
+                ptx::tmem_ld_32x32b_x16(tmem + lane_base + (uint32_t)(buf * S::D_COLS + c0), v);
                 ptx::tmem_wait_ld();
             };
             auto drained = [&]() {
