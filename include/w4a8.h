@@ -436,13 +436,16 @@ W4A8_API w4a8_status w4g_linear_q(const int8_t *Xq, int M, int K, int ldq, const
  * finite. A bfloat16 output is rounded once, from float32. In the gradients
  * each dz / sw is rounded to FP16 relative to a power of two of its row
  * (2^-11 of the value) for bfloat16 rows, and held in two FP16 terms (2^-22)
- * for float32 rows; sums are float32.
+ * for float32 rows; sums are float32. Every call repeats bit for bit.
  *
  * 1 <= K <= W4A8_ACT_MAX_K. flags: W4A8_IO_* | W4A8_STATIC_WEIGHTS | one
- * W4A8_PATH_*: AUTO, GENERIC, and where listed DECODE or TC (forced, for
- * tests; W4A8_ERR_UNSUPPORTED where the form does not exist). Outputs must not
- * overlap inputs, except that Y may be the residual itself (same pointer and
- * stride). M == 0 enqueues nothing but the zeros of the bias gradients.
+ * W4A8_PATH_*: AUTO picks by shape; forced (tests): GENERIC (CUDA cores), TC
+ * (tensor cores), and for the forward calls DECODE (M <= 16, rows that fit a
+ * block's shared memory); W4A8_ERR_UNSUPPORTED where the form cannot run the
+ * shape. Outputs must not overlap inputs or the workspace, except that Y may
+ * be the residual itself (same pointer and stride). Calls that can overlap on
+ * the GPU need workspaces of their own. M == 0 enqueues nothing but the zeros
+ * of the bias gradients.
  */
 #define W4A8_ACT_NONE      0
 #define W4A8_ACT_RELU      1
@@ -497,7 +500,6 @@ W4A8_API w4a8_status w4a8_glu(const void *X, int M, int K, int ldx,
  *   dY [M][lddy]; Z [M][ldz] as saved (ignored, and may be NULL, for
  *   W4A8_ACT_NONE); Wp/ldp/sw as in the forward call.
  *   dX [M][lddx] out, M rows of K.   dbias [N] float32 out, or NULL.
- * Results repeat bit for bit from call to call.
  */
 W4A8_API w4a8_status w4a8_linear_act_grad(const void *dY, int M, int N, int lddy, const void *Z, int ldz,
                                           const uint8_t *Wp, int ldp, const float *sw, int K, int act,
@@ -516,12 +518,13 @@ W4A8_API w4a8_status w4a8_glu_grad(const void *dH, int M, int N, int lddh, const
 
 /* Which kernel path (W4A8_PATH_GENERIC / _DECODE / _TC) the calling thread's
  * last successful w4a8_linear / w4a8_linear_q / w8a8_linear / w8a8_linear_q
- * call enqueued (grouped calls: _DECODE); 0 if none. */
+ * call or MLP call enqueued (grouped calls: _DECODE); 0 if none. */
 W4A8_API unsigned w4a8_last_path(void);
 
 /* How many kernels the calling thread's last successful w4a8_linear /
  * w4a8_linear_q / w4a8_linear_noalloc / w4a8_linear_chain call enqueued
- * (1 to 3; 0 if none, or if that call had M == 0). */
+ * (1 to 3; 0 if none, or if that call had M == 0). MLP calls: 1 to 5 (row
+ * pass, product, join of shared tiles; bias gradients and their sum). */
 W4A8_API unsigned w4a8_last_launch_count(void);
 
 /* Name of the product kernel that the calling thread's last successful
@@ -529,7 +532,8 @@ W4A8_API unsigned w4a8_last_launch_count(void);
  * w4a8_linear_grouped / w8a8_linear / w8a8_linear_q
  * call enqueued ("k_decode_split", "k_decode_ring", "k_linear_decode",
  * "k_gemm_tc", "k_linear_generic", "k_decode_grouped", or for the W8A8 calls
- * "k_linear8_decode", "k_linear8_generic", "k_gemm_tc"), not counting the activation
+ * "k_linear8_decode", "k_linear8_generic", "k_gemm_tc"; MLP calls
+ * "k_mlp_pair", "k_mlp_decode", "k_mlp_simt", "k_grad_simt"), not counting the activation
  * pass; "" if none, or if that call had nothing to do. A static string that
  * the caller must not free. */
 W4A8_API const char *w4a8_last_kernel(void);

@@ -86,7 +86,9 @@ w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a
     unsigned path = flags & W4A8_PATH_MASK;
     const mlp::DecPlan dec = mlp::dec_plan(M, K, N, GLU ? 8 : 16, sms);
     if (path == W4A8_PATH_AUTO)
-        path = mlp_tiny(M, K, N, GLU ? 2 : 1) ? W4A8_PATH_GENERIC : dec.ok ? W4A8_PATH_DECODE : W4A8_PATH_TC;
+        path = mlp_tiny(M, K, N, GLU ? 2 : 1) ? W4A8_PATH_GENERIC
+               : dec.preferred                     ? W4A8_PATH_DECODE
+                                                   : W4A8_PATH_TC;
     if (path != W4A8_PATH_GENERIC && path != W4A8_PATH_DECODE && path != W4A8_PATH_TC) return W4A8_ERR_UNSUPPORTED;
     if (path == W4A8_PATH_DECODE && !dec.ok) return W4A8_ERR_UNSUPPORTED;
     if (path != W4A8_PATH_GENERIC && tc::encode_fn() == nullptr) return W4A8_ERR_UNSUPPORTED;

@@ -314,7 +314,8 @@ k_mlp_decode(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ C
 // ------------------------------------------------------------- host side ---
 
 struct DecPlan {
-    bool ok;
+    bool ok;        // the kernel can run the shape
+    bool preferred; // and is faster than the tensor-core form
     int units;      // FUSED: units of 8 values per thread and row (1, 2, 4, 8), 0: INT8 rows
     int rows;       // FUSED: M rounded up to a power of two
     int grid, ring, max_sb;
@@ -346,6 +347,11 @@ inline DecPlan dec_plan(int M, int K, int N, int ch, int sms) {
             if (fit < 2 || fit * geo.stage_bytes() <= best) continue;
             best = fit * geo.stage_bytes();
             d.ok = true;
+            // Past 8 rows (two MMAs a chunk) one block per SM falls behind the
+            // tensor cores on long layers: 39.7 against 22.6 us at M = 16,
+            // K = 4096, N = 28672; two blocks (22.9 / 23.0 at M = 9) or a layer
+            // of two groups per SM (10.7 / 12.4 at N = 4096) do not.
+            d.preferred = M <= 8 || per_sm == 2 || groups <= 2LL * sms;
             d.grid = (int)grid;
             d.ring = (int)ring;
             d.max_sb = max_sb;

@@ -1040,11 +1040,13 @@ k_mlp_join(const PairArgs p, int npairs) {
 // with fewer SMs the pairs run one after another, none waits for another.
 constexpr int PAIRS = 74;
 
-// Token tile and sharing of a call, by estimated time: rounds of whole tiles,
-// or equal runs of stages plus the join. Measured per stage of 8 MMAs: about
-// 760 ns with 256 tokens, 540 with 128, 600 with 64; the last tile's epilogue
-// about 5 us per 256 tokens; sharing costs the join's launch, the partial
-// tiles written and read (2 x 74 slots; some 16 us with 256 tokens), and it is taken
+// Token tile and sharing of a call, by estimated time. Whole tiles: the first
+// tile's stages, then per round the longer of a tile's stages and its epilogue
+// (beside the next one's stages), then the last epilogue. Measured per stage
+// of 8 MMAs: about 750 ns with 256 tokens, 460 with 128, 400 with 64 (the
+// float32 gradient's a quarter more); the epilogue about 26 ns a token and
+// 0.8 us a tile. Shared: equal runs of stages, the join's launch, the partial
+// tiles written and read (2 x 74 slots; some 16 us with 256 tokens); taken
 // only where the estimate gains a tenth: with long sums the card's power
 // limit, not the idle pairs, sets the pace (2048 x 28672 x 4096: 210 us shared,
 // whole tiles 188).
@@ -1057,18 +1059,19 @@ inline PairPlan pair_plan(int M, int rows, int tile_rows, int stages, bool two =
     PairPlan best = {256, false, 0};
     double best_t = -1.0;
     const int cand[3] = {256, 128, 64};
-    const double stage_ns[3] = {760.0, 540.0, 600.0};
+    const double stage_ns[3] = {750.0, 460.0, 400.0};
     for (int i = two ? 1 : 0; i < 3; ++i) {  // two planes: the sums of 256 tokens do not fit the registers
         const int nt = cand[i];
         const long long tiles = (long long)((M + nt - 1) / nt) * ((rows + tile_rows - 1) / tile_rows);
-        const double whole = (double)((tiles + PAIRS - 1) / PAIRS) * stages * stage_ns[i] + 20.0 * nt;
+        const double main = stages * stage_ns[i], epi = 800.0 + 26.0 * nt;
+        const double whole = main + (double)((tiles - 1) / PAIRS) * (main > epi ? main : epi) + epi;
         if (best_t < 0 || whole < best_t) {
             best_t = whole;
             best = {nt, false, 0};
         }
         const size_t slot = (size_t)256 * nt * 4;
-        const double share = 1.1 * ((double)((tiles * stages + PAIRS - 1) / PAIRS) * stage_ns[i] + 20.0 * nt +
-                                     3000.0 + 16000.0 * nt / 256.0);
+        const double share = 1.1 * ((double)((tiles * stages + PAIRS - 1) / PAIRS) * stage_ns[i] + 2.0 * epi +
+                                    3000.0 + 16000.0 * nt / 256.0);
         if (tiles * stages >= PAIRS && share < best_t) {
             best_t = share;
             best = {nt, true, 2 * PAIRS * slot};
