@@ -10,76 +10,64 @@ from w4a8_quantized_gemm_channel_b200 import native
 lib = native.lib
 
 
-def _linear(**kw):
-    a = dict(X=16, M=4, K=64, ldx=64, Wp=4096, ldp=32, sw=8192, N=8, bias=None, act=0, R=None, ldr=0, flags=0,
-             Y=12288, ldy=8, Z=None, ldz=0, ws=16384, wsb=1 << 20)
-    a.update(kw)
-    return lib.w4a8_linear_act(*a.values(), None)
+ARGS = {
+    "w4a8_linear_act": dict(X=16, M=4, K=64, ldx=64, Wp=4096, ldp=32, sw=8192, N=8, bias=None, act=0, R=None, ldr=0,
+                            flags=0, Y=12288, ldy=8, Z=None, ldz=0, ws=16384, wsb=1 << 20),
+    "w4a8_glu": dict(X=16, M=4, K=64, ldx=64, Wg=4096, sg=8192, Wu=4608, su=8704, ldp=32, N=8, bg=None, bu=None,
+                     act=2, flags=0, H=12288, ldh=8, G=None, U=None, ldgu=0, ws=16384, wsb=1 << 20),
+    "w4a8_linear_act_grad": dict(dY=16, M=4, N=8, lddy=8, Z=1024, ldz=8, Wp=4096, ldp=32, sw=8192, K=64, act=2,
+                                 flags=0, dX=12288, lddx=64, db=None, ws=16384, wsb=1 << 20),
+    "w4a8_glu_grad": dict(dH=16, M=4, N=8, lddh=8, G=1024, U=2048, ldgu=8, Wg=4096, sg=8192, Wu=4608, su=8704,
+                          ldp=32, K=64, act=2, flags=0, dX=12288, lddx=64, dbg=None, dbu=None, ws=16384, wsb=1 << 20),
+}
 
 
-def _glu(**kw):
-    a = dict(X=16, M=4, K=64, ldx=64, Wg=4096, sg=8192, Wu=4608, su=8704, ldp=32, N=8, bg=None, bu=None, act=2,
-             flags=0, H=12288, ldh=8, G=None, U=None, ldgu=0, ws=16384, wsb=1 << 20)
-    a.update(kw)
-    return lib.w4a8_glu(*a.values(), None)
+def call(name, **kw):
+    """The C call on made-up addresses; every case here must be refused before
+    they are used. Strides that the call does not have are dropped."""
+    a = dict(ARGS[name])
+    a.update({k: v for k, v in kw.items() if k in a or not k.startswith("ld")})
+    assert len(a) == len(ARGS[name]), kw
+    return getattr(lib, name)(*a.values(), None)
 
 
-def _linear_grad(**kw):
-    a = dict(dY=16, M=4, N=8, lddy=8, Z=1024, ldz=8, Wp=4096, ldp=32, sw=8192, K=64, act=2, flags=0, dX=12288,
-             lddx=64, db=None, ws=16384, wsb=1 << 20)
-    a.update(kw)
-    return lib.w4a8_linear_act_grad(*a.values(), None)
-
-
-def _glu_grad(**kw):
-    a = dict(dH=16, M=4, N=8, lddh=8, G=1024, U=2048, ldgu=8, Wg=4096, sg=8192, Wu=4608, su=8704, ldp=32, K=64,
-             act=2, flags=0, dX=12288, lddx=64, dbg=None, dbu=None, ws=16384, wsb=1 << 20)
-    a.update(kw)
-    return lib.w4a8_glu_grad(*a.values(), None)
-
-
+LIN, GLU, LIN_GRAD, GLU_GRAD = ARGS
 COMMON = [(dict(K=0), 1), (dict(N=0), 1), (dict(M=-1), 1), (dict(K=131073, ldx=1 << 20, lddx=1 << 20, ldp=1 << 17), 1),
+          (dict(N=1 << 30, ldy=1 << 30, ldh=1 << 30, lddy=1 << 30, lddh=1 << 30), 1), (dict(M=1 << 30), 1),
           (dict(ldp=16), 1), (dict(ldp=40), 1), (dict(act=5), 1), (dict(act=-1), 1),
           (dict(flags=0x01), 1), (dict(flags=0x02), 1), (dict(flags=0x04), 1), (dict(flags=0x200), 1),
           (dict(ws=None), 3), (dict(wsb=10), 3), (dict(ws=16392), 3)]
 
 
-def _known(fn, kw):
-    # each call takes the arguments it has
-    names = fn.__code__.co_consts
-    return {k: v for k, v in kw.items() if k not in ("ldx", "lddx") or any(
-        isinstance(c, tuple) and k in c for c in names)}
-
-
-@pytest.mark.parametrize("fn", [_linear, _glu, _linear_grad, _glu_grad])
+@pytest.mark.parametrize("name", ARGS)
 @pytest.mark.parametrize("kw,want", COMMON)
-def test_sizes_flags_and_workspace(fn, kw, want):
-    assert fn(**_known(fn, kw)) == want
+def test_sizes_flags_and_workspace(name, kw, want):
+    assert call(name, **kw) == want
 
 
-@pytest.mark.parametrize("fn,kw", [
-    (_linear, dict(X=None)), (_linear, dict(Y=None)), (_linear, dict(Wp=None)), (_linear, dict(sw=None)),
-    (_linear, dict(Wp=4104)), (_linear, dict(sw=8193)), (_linear, dict(bias=2)), (_linear, dict(ldx=63)),
-    (_linear, dict(ldy=7)), (_linear, dict(R=64, ldr=7)), (_linear, dict(R=66, ldr=8)), (_linear, dict(Z=64, ldz=7)),
-    (_linear, dict(X=17, flags=0x100)), (_linear, dict(X=18)),
-    (_glu, dict(X=None)), (_glu, dict(H=None)), (_glu, dict(Wg=None)), (_glu, dict(Wu=None)), (_glu, dict(su=None)),
-    (_glu, dict(Wu=4616)), (_glu, dict(bu=2)), (_glu, dict(G=64, ldgu=8)), (_glu, dict(U=64, ldgu=8)),
-    (_glu, dict(G=64, U=1024, ldgu=7)), (_glu, dict(ldh=7)), (_glu, dict(G=65, U=1024, ldgu=8, flags=0x100)),
-    (_linear_grad, dict(dY=None)), (_linear_grad, dict(Z=None)), (_linear_grad, dict(dX=None)),
-    (_linear_grad, dict(lddy=7)), (_linear_grad, dict(ldz=7)), (_linear_grad, dict(lddx=63)),
-    (_linear_grad, dict(db=2)), (_linear_grad, dict(sw=None)),
-    (_glu_grad, dict(dH=None)), (_glu_grad, dict(G=None)), (_glu_grad, dict(U=None)), (_glu_grad, dict(ldgu=7)),
-    (_glu_grad, dict(dX=None)), (_glu_grad, dict(dbu=2)), (_glu_grad, dict(su=None)),
+@pytest.mark.parametrize("name,kw", [
+    (LIN, dict(X=None)), (LIN, dict(Y=None)), (LIN, dict(Wp=None)), (LIN, dict(sw=None)),
+    (LIN, dict(Wp=4104)), (LIN, dict(sw=8193)), (LIN, dict(bias=2)), (LIN, dict(ldx=63)),
+    (LIN, dict(ldy=7)), (LIN, dict(R=64, ldr=7)), (LIN, dict(R=66, ldr=8)), (LIN, dict(Z=64, ldz=7)),
+    (LIN, dict(X=17, flags=0x100)), (LIN, dict(X=18)),
+    (GLU, dict(X=None)), (GLU, dict(H=None)), (GLU, dict(Wg=None)), (GLU, dict(Wu=None)), (GLU, dict(su=None)),
+    (GLU, dict(Wu=4616)), (GLU, dict(bu=2)), (GLU, dict(G=64, ldgu=8)), (GLU, dict(U=64, ldgu=8)),
+    (GLU, dict(G=64, U=1024, ldgu=7)), (GLU, dict(ldh=7)), (GLU, dict(G=65, U=1024, ldgu=8, flags=0x100)),
+    (LIN_GRAD, dict(dY=None)), (LIN_GRAD, dict(Z=None)), (LIN_GRAD, dict(dX=None)),
+    (LIN_GRAD, dict(lddy=7)), (LIN_GRAD, dict(ldz=7)), (LIN_GRAD, dict(lddx=63)),
+    (LIN_GRAD, dict(db=2)), (LIN_GRAD, dict(sw=None)),
+    (GLU_GRAD, dict(dH=None)), (GLU_GRAD, dict(G=None)), (GLU_GRAD, dict(U=None)), (GLU_GRAD, dict(ldgu=7)),
+    (GLU_GRAD, dict(dX=None)), (GLU_GRAD, dict(dbu=2)), (GLU_GRAD, dict(su=None)),
 ])
-def test_pointers_and_strides(fn, kw):
-    assert fn(**kw) == native.ERR_INVALID_ARG
+def test_pointers_and_strides(name, kw):
+    assert call(name, **kw) == native.ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("fn", [_linear, _glu, _linear_grad, _glu_grad])
-def test_no_rows_and_no_device(fn):
-    assert fn(M=0, ws=None, wsb=0) == native.OK
+@pytest.mark.parametrize("name", ARGS)
+def test_no_rows_and_no_device(name):
+    assert call(name, M=0, ws=None, wsb=0) == native.OK
     if not torch.cuda.is_available():
-        assert fn() == native.ERR_UNSUPPORTED
+        assert call(name) == native.ERR_UNSUPPORTED
 
 
 def test_workspace_sizes():

@@ -22,6 +22,7 @@ inline bool io_vec(const void *p, int ld, unsigned flags) {
 // What every MLP call checks about sizes, flags and one projection.
 w4a8_status check_mlp(int M, int K, int N, int ldp, int act, unsigned flags) {
     if (M < 0 || K < 1 || K > W4A8_ACT_MAX_K || N < 1) return W4A8_ERR_INVALID_ARG;
+    if (M >= 1 << 30 || N >= 1 << 30) return W4A8_ERR_INVALID_ARG;  // two of them fit an int
     if (ldp < (K + 1) / 2 || ldp % 16 != 0) return W4A8_ERR_INVALID_ARG;
     if (act < W4A8_ACT_NONE || act > W4A8_ACT_GELU_TANH) return W4A8_ERR_INVALID_ARG;
     if (flags & ~(W4A8_IO_BF16 | W4A8_STATIC_WEIGHTS | W4A8_PATH_MASK)) return W4A8_ERR_INVALID_ARG;
@@ -211,8 +212,8 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
             }
             if (e != cudaSuccess) return (w4a8_status)W4A8_ERR_CUDA;
         }
-        const int bytes = SEGS * ws.seg * (int)sizeof(float);
-        const bool held = bytes <= mlp::GR_HELD_MAX;
+        const size_t bytes = (size_t)SEGS * ws.seg * sizeof(float);
+        const bool held = bytes <= (size_t)mlp::GR_HELD_MAX;
         auto kern = held ? mlp::k_grad_rows<GLU, LO, true, ACT, T> : mlp::k_grad_rows<GLU, LO, false, ACT, T>;
         if (held && !raise_smem_limit(reinterpret_cast<const void *>(kern), mlp::GR_HELD_MAX))
             return (w4a8_status)W4A8_ERR_CUDA;
