@@ -493,38 +493,53 @@ def _mlp_flags(rows: torch.Tensor, act: str, path: str, static_weights: bool):
                          f"{', '.join(_PATH)}; got {e}") from None
 
 
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Row stride of a 2-D tensor with unit column stride. torch gives no
-    meaning to the stride of a single row or column."""
+def _row_stride(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
+    """Row stride of a [rows][cols] tensor with unit column stride. torch gives
+    no meaning to the stride of a single row or column."""
     ld, one = t.stride()
-    rows, cols = t.shape
     if one != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
     return ld if rows > 1 else max(ld, cols)
 
 
-def _like(t: torch.Tensor | None, name: str, dtype, device, shape) -> int:
-    """Row stride of an optional row tensor of this type, device and shape (0 for None)."""
+def _rows_in(t: torch.Tensor, name: str):
+    """(rows, columns, row stride, device index) of a call's leading row tensor."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    m, n = t.shape
+    return m, n, _row_stride(t, name, m, n), t.get_device()
+
+
+def _like(t: torch.Tensor | None, name: str, x: torch.Tensor, dev: int, m: int, n: int) -> int:
+    """Row stride of an optional [m][n] tensor of x's type and device (0 for None)."""
     if t is None:
         return 0
-    if t.dtype != dtype or t.device != device or t.shape != shape:
-        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on {device}")
-    return _row_stride(t, name)
+    if t.dtype != x.dtype or t.get_device() != dev or t.shape != (m, n):
+        raise ValueError(f"{name} must be a [{m}][{n}] {x.dtype} tensor on {x.device}")
+    return _row_stride(t, name, m, n)
 
 
-def _codes(wp: torch.Tensor, name: str, k: int, device):
-    """(N, row stride) of packed codes [N][>= packed_ld(k)]."""
-    if wp.dtype != torch.uint8 or wp.device != device or wp.dim() != 2 or wp.shape[1] < (k + 1) // 2:
-        raise ValueError(f"{name} must be [N][>= {packed_ld(k)}] packed uint8 codes for K = {k} on {device}")
-    return wp.shape[0], _row_stride(wp, name)
+def _codes(wp: torch.Tensor, name: str, k: int, dev: int):
+    """(N, row stride) of packed codes [N][>= ceil(k / 2)]."""
+    if wp.dtype != torch.uint8 or wp.get_device() != dev or wp.dim() != 2 or wp.shape[1] < (k + 1) // 2:
+        raise ValueError(f"{name} must be [N][>= {packed_ld(k)}] packed uint8 codes for K = {k} on device {dev}")
+    n, cols = wp.shape
+    return n, _row_stride(wp, name, n, cols)
 
 
-def _vector(t: torch.Tensor | None, name: str, n: int, device) -> int | None:
+def _pair(wg, wu, k: int, dev: int):
+    n, ldp = _codes(wg, "wg", k, dev)
+    if _codes(wu, "wu", k, dev) != (n, ldp):
+        raise ValueError("the two projections must have the same shape and row stride")
+    return n, ldp
+
+
+def _vector(t: torch.Tensor | None, name: str, n: int, dev: int) -> int | None:
     """Address of a float32 vector of n values (None for None)."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.device != device or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} values on {device}")
+    if t.dtype != torch.float32 or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} values on device {dev}")
     return t.data_ptr()
 
 
@@ -532,24 +547,18 @@ def _at(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _two_dim(t: torch.Tensor, name: str):
-    if t.dim() != 2 or not t.is_cuda:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    return t.shape
-
-
-def _mlp_call(fn, what: str, device, size, args, workspace, stream):
-    """fn(*args, workspace, bytes, stream) with the rows' device current."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _mlp_call(fn, what, device, size, args, workspace, stream)
+def _mlp_call(fn, what: str, x: torch.Tensor, dev: int, size, args, workspace, stream):
+    """fn(*args, workspace, bytes, stream) with x's device current."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _mlp_call(fn, what, x, dev, size, args, workspace, stream)
     if workspace is None:
-        workspace = torch.empty(max(size(), 1), dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {device}")
-    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+        workspace = torch.empty(max(size(), 1), dtype=torch.uint8, device=x.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {x.device}")
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     status = fn(*args, workspace.data_ptr(), workspace.nbytes, s)
-    if status != OK:
+    if status:
         raise W4A8Error(status, what)
 
 
@@ -569,18 +578,13 @@ def w4a8_linear_act(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, bias: t
     X's dtype. With save (or z given) returns (Y, Z), Z the pre-activations
     that w4a8_linear_act_grad reads. y may be the residual itself."""
     flags, code = _mlp_flags(x, act, path, static_weights)
-    m, k = _two_dim(x, "X")
-    dt, dev = x.dtype, x.device
+    m, k, ldx, dev = _rows_in(x, "X")
     n, ldp = _codes(wp, "wp", k, dev)
-    if y is None:
-        y = torch.empty((m, n), dtype=dt, device=dev)
-    if save and z is None:
-        z = torch.empty((m, n), dtype=dt, device=dev)
-    shape = (m, n)
-    ldy, ldz, ldr = (_like(y, "Y", dt, dev, shape), _like(z, "Z", dt, dev, shape),
-                     _like(residual, "residual", dt, dev, shape))
-    _mlp_call(lib.w4a8_linear_act, "w4a8_linear_act", dev, lambda: act_workspace_size(m, k, n, 1, dt),
-              (x.data_ptr(), m, k, _row_stride(x, "X"), wp.data_ptr(), ldp, _vector(sw, "sw", n, dev), n,
+    y, ldy = (x.new_empty((m, n)), n) if y is None else (y, _like(y, "Y", x, dev, m, n))
+    z, ldz = (x.new_empty((m, n)), n) if save and z is None else (z, _like(z, "Z", x, dev, m, n))
+    ldr = _like(residual, "residual", x, dev, m, n)
+    _mlp_call(lib.w4a8_linear_act, "w4a8_linear_act", x, dev, lambda: act_workspace_size(m, k, n, 1, x.dtype),
+              (x.data_ptr(), m, k, ldx, wp.data_ptr(), ldp, _vector(sw, "sw", n, dev), n,
                _vector(bias, "bias", n, dev), code, _at(residual), ldr, flags, y.data_ptr(), ldy, _at(z), ldz),
               workspace, stream)
     return y if z is None else (y, z)
@@ -595,29 +599,20 @@ def w4a8_glu(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, wu: torch.Tens
     of X with their biases. With save (or g and u given) returns (H, G, U) for
     w4a8_glu_grad."""
     flags, code = _mlp_flags(x, act, path, static_weights)
-    m, k = _two_dim(x, "X")
-    dt, dev = x.dtype, x.device
+    m, k, ldx, dev = _rows_in(x, "X")
     n, ldp = _pair(wg, wu, k, dev)
-    if h is None:
-        h = torch.empty((m, n), dtype=dt, device=dev)
+    h, ldh = (x.new_empty((m, n)), n) if h is None else (h, _like(h, "H", x, dev, m, n))
     if save and g is None and u is None:
-        g, u = (torch.empty((m, n), dtype=dt, device=dev) for _ in range(2))
-    ldh, ldg, ldu = (_like(h, "H", dt, dev, (m, n)), _like(g, "G", dt, dev, (m, n)), _like(u, "U", dt, dev, (m, n)))
+        g, u = x.new_empty((m, n)), x.new_empty((m, n))
+    ldg, ldu = _like(g, "G", x, dev, m, n), _like(u, "U", x, dev, m, n)
     if ldg != ldu:
         raise ValueError("G and U must both be given, with one row stride")
-    _mlp_call(lib.w4a8_glu, "w4a8_glu", dev, lambda: act_workspace_size(m, k, n, 2, dt),
-              (x.data_ptr(), m, k, _row_stride(x, "X"), wg.data_ptr(), _vector(sg, "sg", n, dev), wu.data_ptr(),
+    _mlp_call(lib.w4a8_glu, "w4a8_glu", x, dev, lambda: act_workspace_size(m, k, n, 2, x.dtype),
+              (x.data_ptr(), m, k, ldx, wg.data_ptr(), _vector(sg, "sg", n, dev), wu.data_ptr(),
                _vector(su, "su", n, dev), ldp, n, _vector(gate_bias, "gate_bias", n, dev),
                _vector(up_bias, "up_bias", n, dev), code, flags, h.data_ptr(), ldh, _at(g), _at(u), ldg),
               workspace, stream)
     return h if g is None else (h, g, u)
-
-
-def _pair(wg, wu, k: int, dev):
-    n, ldp = _codes(wg, "wg", k, dev)
-    if _codes(wu, "wu", k, dev) != (n, ldp):
-        raise ValueError("the two projections must have the same shape and row stride")
-    return n, ldp
 
 
 def w4a8_linear_act_grad(dy: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, k: int, act: str = "none",
@@ -628,20 +623,19 @@ def w4a8_linear_act_grad(dy: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, k
     dtype; z is the saved pre-activations (not needed without activation).
     The residual's gradient is dY."""
     flags, code = _mlp_flags(dy, act, path, static_weights)
-    m, n = _two_dim(dy, "dY")
-    dt, dev = dy.dtype, dy.device
+    m, n, lddy, dev = _rows_in(dy, "dY")
     rows, ldp = _codes(wp, "wp", k, dev)
     if rows != n:
         raise ValueError(f"dY must have {rows} columns")
     if act == "none":
         z = None
-    if dx is None:
-        dx = torch.empty((m, k), dtype=dt, device=dev)
-    ldz, lddx = _like(z, "Z", dt, dev, (m, n)), _like(dx, "dX", dt, dev, (m, k))
-    db = torch.empty(n, dtype=torch.float32, device=dev) if bias_grad else None
-    _mlp_call(lib.w4a8_linear_act_grad, "w4a8_linear_act_grad", dev, lambda: grad_workspace_size(m, k, n, 1, dt),
-              (dy.data_ptr(), m, n, _row_stride(dy, "dY"), _at(z), ldz, wp.data_ptr(), ldp,
-               _vector(sw, "sw", n, dev), k, code, flags, dx.data_ptr(), lddx, _at(db)), workspace, stream)
+    dx, lddx = (dy.new_empty((m, k)), k) if dx is None else (dx, _like(dx, "dX", dy, dev, m, k))
+    ldz = _like(z, "Z", dy, dev, m, n)
+    db = torch.empty(n, dtype=torch.float32, device=dy.device) if bias_grad else None
+    _mlp_call(lib.w4a8_linear_act_grad, "w4a8_linear_act_grad", dy, dev,
+              lambda: grad_workspace_size(m, k, n, 1, dy.dtype),
+              (dy.data_ptr(), m, n, lddy, _at(z), ldz, wp.data_ptr(), ldp, _vector(sw, "sw", n, dev), k, code, flags,
+               dx.data_ptr(), lddx, _at(db)), workspace, stream)
     return (dx, db) if bias_grad else dx
 
 
@@ -652,21 +646,19 @@ def w4a8_glu_grad(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, wg: torch.
     """dX[M][k] (and with bias_grad the two bias gradients [N]) of w4a8_glu,
     of dH's dtype, from the saved G and U."""
     flags, code = _mlp_flags(dh, act, path, static_weights)
-    m, n = _two_dim(dh, "dH")
-    dt, dev = dh.dtype, dh.device
+    m, n, lddh, dev = _rows_in(dh, "dH")
     rows, ldp = _pair(wg, wu, k, dev)
     if rows != n:
         raise ValueError(f"dH must have {rows} columns")
-    if dx is None:
-        dx = torch.empty((m, k), dtype=dt, device=dev)
-    ldg, ldu, lddx = (_like(g, "G", dt, dev, (m, n)), _like(u, "U", dt, dev, (m, n)), _like(dx, "dX", dt, dev, (m, k)))
+    dx, lddx = (dh.new_empty((m, k)), k) if dx is None else (dx, _like(dx, "dX", dh, dev, m, k))
+    ldg, ldu = _like(g, "G", dh, dev, m, n), _like(u, "U", dh, dev, m, n)
     if ldg != ldu or g is None:
         raise ValueError("G and U must both be given, with one row stride")
-    dbg, dbu = (torch.empty(n, dtype=torch.float32, device=dev) if bias_grad else None for _ in range(2))
-    _mlp_call(lib.w4a8_glu_grad, "w4a8_glu_grad", dev, lambda: grad_workspace_size(m, k, n, 2, dt),
-              (dh.data_ptr(), m, n, _row_stride(dh, "dH"), g.data_ptr(), u.data_ptr(), ldg, wg.data_ptr(),
-               _vector(sg, "sg", n, dev), wu.data_ptr(), _vector(su, "su", n, dev), ldp, k, code, flags,
-               dx.data_ptr(), lddx, _at(dbg), _at(dbu)), workspace, stream)
+    dbg, dbu = (torch.empty(n, dtype=torch.float32, device=dh.device) if bias_grad else None for _ in range(2))
+    _mlp_call(lib.w4a8_glu_grad, "w4a8_glu_grad", dh, dev, lambda: grad_workspace_size(m, k, n, 2, dh.dtype),
+              (dh.data_ptr(), m, n, lddh, g.data_ptr(), u.data_ptr(), ldg, wg.data_ptr(), _vector(sg, "sg", n, dev),
+               wu.data_ptr(), _vector(su, "su", n, dev), ldp, k, code, flags, dx.data_ptr(), lddx, _at(dbg),
+               _at(dbu)), workspace, stream)
     return (dx, dbg, dbu) if bias_grad else dx
 
 
