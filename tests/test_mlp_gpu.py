@@ -399,3 +399,52 @@ def test_longest_sums():
         native.w4a8_linear_act(torch.zeros(1, k + 1, device="cuda"),
                                torch.zeros(1, native.packed_ld(k + 1), dtype=torch.uint8, device="cuda"),
                                torch.ones(1, device="cuda"))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [520, 523])
+def test_shared_tiles(io, n):
+    """Long sums over few tiles: the pairs share the stages out and a third
+    launch joins the parts and finishes, whatever the epilogue."""
+    m, k = 40, 16390
+    rnd = gen(n)
+    (qg, sg, wg), (qu, su, wu) = weights(rnd, n, k), weights(rnd, n, k)
+    x, r, b1, b2 = rows(rnd, m, k, DT[io]), rnd(m, n, std=2.0).to(DT[io]), rnd(n), rnd(n)
+    for act in ACTS:
+        got = native.w4a8_linear_act(x, wg, sg, bias=b1, act=act, residual=r, save=True, path="tc")
+        assert native.last_launch_count() == 3
+        for t, (w, e), what in zip(got, ref.linear(x, qg, sg, b1, act, r), "yz"):
+            ref.check(t, w, e, f"{what} {act}")
+        got = native.w4a8_glu(x, wg, sg, wu, su, gate_bias=b1, up_bias=b2, act=act, save=True, path="tc")
+        assert native.last_launch_count() == 3
+        for t, (w, e), what in zip(got, ref.glu(x, qg, sg, qu, su, b1, b2, act), "hgu"):
+            ref.check(t, w, e, f"{what} {act}")
+    dh = rnd(m, k, std=0.01).to(DT[io])       # the same layer the other way round: N and K exchanged
+    q, sw, wp = weights(rnd, k, n)
+    got = native.w4a8_linear_act_grad(dh, wp, sw, n)
+    assert native.last_launch_count() == 3
+    ref.check(got, *ref.linear_grad(dh, dh, q, sw, "none", True)[0], "dx")
+
+
+def test_two_streams_at_once():
+    """Blocks running on two streams at the same time, each with its own
+    buffers, give the bits they give alone."""
+    d, f = 512, 1300
+    rnd = gen(31)
+    p = {}
+    for name, (n, k) in dict(g=(f, d), u=(f, d), d=(d, f)).items():
+        _, sw, wp = weights(rnd, n, k)
+        p[name] = (wp, sw)
+    xs = [rows(rnd, m, d, dt) for m, dt in ((300, torch.bfloat16), (5, torch.float32))]
+    alone = [block(x, p, "silu") for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    both = []
+    for _ in range(20):
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                both.append(block(x, p, "silu"))
+    torch.cuda.synchronize()
+    for i, out in enumerate(both):
+        for a, b in zip(alone[i % 2], out):
+            assert torch.equal(a, b)
