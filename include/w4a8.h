@@ -438,13 +438,14 @@ W4A8_API w4a8_status w4g_linear_q(const int8_t *Xq, int M, int K, int ldq, const
  * (2^-11 of the value) for bfloat16 rows, and held in two FP16 terms (2^-22)
  * for float32 rows; sums are float32. Every call repeats bit for bit.
  *
- * 1 <= K <= W4A8_ACT_MAX_K; M and N below 2^30. flags: W4A8_IO_* | W4A8_STATIC_WEIGHTS | one
- * W4A8_PATH_*: AUTO picks by shape; forced (tests): GENERIC (CUDA cores), TC
- * (tensor cores), and for the forward calls DECODE (M <= 16, rows that fit a
- * block's shared memory); W4A8_ERR_UNSUPPORTED where the form cannot run the
- * shape. Outputs must not overlap inputs or the workspace, except that Y may
- * be the residual itself (same pointer and stride). Calls that can overlap on
- * the GPU need workspaces of their own. M == 0 enqueues nothing but the zeros
+ * 1 <= K <= W4A8_ACT_MAX_K; M and N below 2^30, N of w4a8_glu_grad at most
+ * 2^30 - 128. flags: W4A8_IO_* | W4A8_STATIC_WEIGHTS | one W4A8_PATH_*: AUTO
+ * picks by shape; forced (tests): GENERIC (CUDA cores), TC (tensor cores), and
+ * for the forward calls DECODE (M <= 16, rows that fit a block's shared
+ * memory); W4A8_ERR_UNSUPPORTED where the form cannot run the shape. Outputs
+ * must not overlap inputs or the workspace, except that Y may be the residual
+ * itself (same pointer and stride). Calls that can overlap on the GPU need
+ * workspaces of their own. M == 0 enqueues nothing but the zeros
  * of the bias gradients.
  */
 #define W4A8_ACT_NONE      0

@@ -3,6 +3,8 @@
 // Included at the end of w4a8_abi.cu, whose helpers it uses.
 #pragma once
 
+#include <climits>
+
 #include "mlp_gemm.cuh"
 #include "mlp_decode.cuh"
 
@@ -32,6 +34,9 @@ w4a8_status check_proj(const uint8_t *Wp, const float *sw, const float *vec) {
     if (!Wp || !sw || !aligned16(Wp) || !aligned4(sw) || (vec && !aligned4(vec))) return W4A8_ERR_INVALID_ARG;
     return W4A8_OK;
 }
+// The gradient's operand rows hold a segment per projection, N rounded up to
+// the product's step of 128; the kernels count their columns in an int.
+bool grad_rows_fit(int N, int segs) { return ((long long)N + 127) / 128 * 128 * segs <= INT_MAX; }
 // A row array of `cols` columns: required ones must be there when there are rows.
 bool rows_ok(const void *p, int ld, int cols, bool required, int M, unsigned flags) {
     if (!p) return !required || M == 0;
@@ -286,6 +291,7 @@ size_t w4a8_act_workspace_size(int M, int K, int N, int projections, unsigned fl
 
 size_t w4a8_grad_workspace_size(int M, int K, int N, int projections, unsigned flags) {
     if (M < 0 || K < 1 || K > W4A8_ACT_MAX_K || N < 1 || projections < 1 || projections > 2) return 0;
+    if (!grad_rows_fit(N, projections)) return 0;
     return grad_layout(M, K, N, projections, flags).total();
 }
 
@@ -343,6 +349,7 @@ w4a8_status w4a8_glu_grad(const void *dH, int M, int N, int lddh, const void *G,
     if (st == W4A8_OK) st = check_proj(Wg, sg, dbg);
     if (st == W4A8_OK) st = check_proj(Wu, su, dbu);
     if (st != W4A8_OK) return st;
+    if (!grad_rows_fit(N, 2)) return W4A8_ERR_INVALID_ARG;
     if (!rows_ok(dH, lddh, N, true, M, flags) || !rows_ok(G, ldgu, N, true, M, flags) ||
         !rows_ok(U, ldgu, N, true, M, flags) || !rows_ok(dX, lddx, K, true, M, flags))
         return W4A8_ERR_INVALID_ARG;
