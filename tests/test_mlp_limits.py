@@ -34,3 +34,12 @@ def test_widest_gradient_rows_workspace():
         assert size >= planes * 2 * TOP * 2                   # FP16 rows of two segments
         assert lib.w4a8_grad_workspace_size(1, 64, TOP + 1, 2, flags) == 0
         assert lib.w4a8_grad_workspace_size(1, 64, TOP + 1, 1, flags) >= planes * TOP * 2
+
+
+@pytest.mark.parametrize("m,k,n,flags", [
+    (1 << 30, 64, 8, 0), (1, 64, 1 << 30, 0), (1, 64, 2 ** 31 - 1, 0), (2 ** 31 - 1, 64, 8, 0),
+    (1, 64, 8, native.RELU), (1, 64, 8, native.OUT_BF16), (1, 64, 8, 0x200)])
+def test_rejected_sizes_and_flags_need_no_workspace(m, k, n, flags):
+    for projections in (1, 2):
+        assert lib.w4a8_act_workspace_size(m, k, n, projections, flags) == 0
+        assert lib.w4a8_grad_workspace_size(m, k, n, projections, flags) == 0

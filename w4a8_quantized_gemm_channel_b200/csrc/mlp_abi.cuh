@@ -21,13 +21,18 @@ inline bool io_vec(const void *p, int ld, unsigned flags) {
     return aligned16(p) && ((size_t)ld * io_size(flags)) % 16 == 0;
 }
 
-// What every MLP call checks about sizes, flags and one projection.
-w4a8_status check_mlp(int M, int K, int N, int ldp, int act, unsigned flags) {
+// What every MLP call, and the size query for it, checks about sizes and flags.
+w4a8_status check_sizes(int M, int K, int N, unsigned flags) {
     if (M < 0 || K < 1 || K > W4A8_ACT_MAX_K || N < 1) return W4A8_ERR_INVALID_ARG;
     if (M >= 1 << 30 || N >= 1 << 30) return W4A8_ERR_INVALID_ARG;  // two of them fit an int
+    if (flags & ~(W4A8_IO_BF16 | W4A8_STATIC_WEIGHTS | W4A8_PATH_MASK)) return W4A8_ERR_INVALID_ARG;
+    return W4A8_OK;
+}
+// What every MLP call checks besides, and about one projection.
+w4a8_status check_mlp(int M, int K, int N, int ldp, int act, unsigned flags) {
+    if (check_sizes(M, K, N, flags) != W4A8_OK) return W4A8_ERR_INVALID_ARG;
     if (ldp < (K + 1) / 2 || ldp % 16 != 0) return W4A8_ERR_INVALID_ARG;
     if (act < W4A8_ACT_NONE || act > W4A8_ACT_GELU_TANH) return W4A8_ERR_INVALID_ARG;
-    if (flags & ~(W4A8_IO_BF16 | W4A8_STATIC_WEIGHTS | W4A8_PATH_MASK)) return W4A8_ERR_INVALID_ARG;
     return W4A8_OK;
 }
 w4a8_status check_proj(const uint8_t *Wp, const float *sw, const float *vec) {
@@ -284,13 +289,12 @@ w4a8_status mlp_grad_call(const void *dY, int M, int N, int lddy, const void *Z,
 extern "C" {
 
 size_t w4a8_act_workspace_size(int M, int K, int N, int projections, unsigned flags) {
-    if (M < 0 || K < 1 || K > W4A8_ACT_MAX_K || N < 1 || projections < 1 || projections > 2) return 0;
-    (void)flags;
+    if (check_sizes(M, K, N, flags) != W4A8_OK || projections < 1 || projections > 2) return 0;
     return forward_workspace(M, K, N, projections == 2);
 }
 
 size_t w4a8_grad_workspace_size(int M, int K, int N, int projections, unsigned flags) {
-    if (M < 0 || K < 1 || K > W4A8_ACT_MAX_K || N < 1 || projections < 1 || projections > 2) return 0;
+    if (check_sizes(M, K, N, flags) != W4A8_OK || projections < 1 || projections > 2) return 0;
     if (!grad_rows_fit(N, projections)) return 0;
     return grad_layout(M, K, N, projections, flags).total();
 }
