@@ -123,6 +123,24 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _under(stream, fn, args: dict):
+    """fn(**args) with `stream` current, so that what it allocates belongs to
+    the stream that uses it: a workspace of another stream's could be handed
+    out again there while this one still reads it. What is returned is noted
+    as used by the caller's stream too."""
+    lead = next(iter(args.values()))
+    if isinstance(lead, torch.Tensor) and lead.is_cuda and lead.device != stream.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {lead.device}")
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = fn(**dict(args, stream=None))
+    if caller != stream:
+        for t in out if isinstance(out, (tuple, list)) else (out,):
+            if t is not None:
+                t.record_stream(caller)
+    return out
+
+
 def _rowmajor(t: torch.Tensor, name: str):
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
@@ -479,7 +497,9 @@ def w4g_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor, s
 # The W4A8 product with bias, activation and residual in its epilogue, the
 # gated feed-forward product, and the input gradients of both. Rows are all
 # float32 or all bfloat16; act is "none", "relu", "silu", "gelu" or
-# "gelu_tanh". Formulas and rules: include/w4a8.h.
+# "gelu_tanh". Formulas and rules: include/w4a8.h. A call runs on `stream`, the
+# current one by default; outputs and workspace that it allocates belong to that
+# stream, and what it reads must be ready there.
 
 # A call on few rows takes the GPU about as long as its marshalling takes the
 # host, so this part keeps to plain integers and checks each fact once.
@@ -547,17 +567,16 @@ def _at(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _mlp_call(fn, what: str, x: torch.Tensor, dev: int, size, args, workspace, stream):
-    """fn(*args, workspace, bytes, stream) with x's device current."""
+def _mlp_call(fn, what: str, x: torch.Tensor, dev: int, size, args, workspace):
+    """fn(*args, workspace, bytes, stream) on the current stream of x's device."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _mlp_call(fn, what, x, dev, size, args, workspace, stream)
+            return _mlp_call(fn, what, x, dev, size, args, workspace)
     if workspace is None:
         workspace = torch.empty(max(size(), 1), dtype=torch.uint8, device=x.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {x.device}")
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    status = fn(*args, workspace.data_ptr(), workspace.nbytes, s)
+    status = fn(*args, workspace.data_ptr(), workspace.nbytes, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         raise W4A8Error(status, what)
 
@@ -577,6 +596,8 @@ def w4a8_linear_act(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, bias: t
     """Y[M][N] = act(dequant(quant8(X) @ unpack(Wp)^T) + bias) + residual, of
     X's dtype. With save (or z given) returns (Y, Z), Z the pre-activations
     that w4a8_linear_act_grad reads. y may be the residual itself."""
+    if stream is not None:
+        return _under(stream, w4a8_linear_act, locals())
     flags, code = _mlp_flags(x, act, path, static_weights)
     m, k, ldx, dev = _rows_in(x, "X")
     n, ldp = _codes(wp, "wp", k, dev)
@@ -586,7 +607,7 @@ def w4a8_linear_act(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, bias: t
     _mlp_call(lib.w4a8_linear_act, "w4a8_linear_act", x, dev, lambda: act_workspace_size(m, k, n, 1, x.dtype),
               (x.data_ptr(), m, k, ldx, wp.data_ptr(), ldp, _vector(sw, "sw", n, dev), n,
                _vector(bias, "bias", n, dev), code, _at(residual), ldr, flags, y.data_ptr(), ldy, _at(z), ldz),
-              workspace, stream)
+              workspace)
     return y if z is None else (y, z)
 
 
@@ -598,6 +619,8 @@ def w4a8_glu(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, wu: torch.Tens
     """H[M][N] = act(G) * U of X's dtype, G and U the gate and up projections
     of X with their biases. With save (or g and u given) returns (H, G, U) for
     w4a8_glu_grad."""
+    if stream is not None:
+        return _under(stream, w4a8_glu, locals())
     flags, code = _mlp_flags(x, act, path, static_weights)
     m, k, ldx, dev = _rows_in(x, "X")
     n, ldp = _pair(wg, wu, k, dev)
@@ -611,7 +634,7 @@ def w4a8_glu(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, wu: torch.Tens
               (x.data_ptr(), m, k, ldx, wg.data_ptr(), _vector(sg, "sg", n, dev), wu.data_ptr(),
                _vector(su, "su", n, dev), ldp, n, _vector(gate_bias, "gate_bias", n, dev),
                _vector(up_bias, "up_bias", n, dev), code, flags, h.data_ptr(), ldh, _at(g), _at(u), ldg),
-              workspace, stream)
+              workspace)
     return h if g is None else (h, g, u)
 
 
@@ -622,6 +645,8 @@ def w4a8_linear_act_grad(dy: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, k
     """dX[M][k] (and with bias_grad dbias[N]) of w4a8_linear_act, of dY's
     dtype; z is the saved pre-activations (not needed without activation).
     The residual's gradient is dY."""
+    if stream is not None:
+        return _under(stream, w4a8_linear_act_grad, locals())
     flags, code = _mlp_flags(dy, act, path, static_weights)
     m, n, lddy, dev = _rows_in(dy, "dY")
     rows, ldp = _codes(wp, "wp", k, dev)
@@ -635,7 +660,7 @@ def w4a8_linear_act_grad(dy: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor, k
     _mlp_call(lib.w4a8_linear_act_grad, "w4a8_linear_act_grad", dy, dev,
               lambda: grad_workspace_size(m, k, n, 1, dy.dtype),
               (dy.data_ptr(), m, n, lddy, _at(z), ldz, wp.data_ptr(), ldp, _vector(sw, "sw", n, dev), k, code, flags,
-               dx.data_ptr(), lddx, _at(db)), workspace, stream)
+               dx.data_ptr(), lddx, _at(db)), workspace)
     return (dx, db) if bias_grad else dx
 
 
@@ -645,6 +670,8 @@ def w4a8_glu_grad(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, wg: torch.
                   stream=None, static_weights: bool = False):
     """dX[M][k] (and with bias_grad the two bias gradients [N]) of w4a8_glu,
     of dH's dtype, from the saved G and U."""
+    if stream is not None:
+        return _under(stream, w4a8_glu_grad, locals())
     flags, code = _mlp_flags(dh, act, path, static_weights)
     m, n, lddh, dev = _rows_in(dh, "dH")
     rows, ldp = _pair(wg, wu, k, dev)
@@ -658,7 +685,7 @@ def w4a8_glu_grad(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, wg: torch.
     _mlp_call(lib.w4a8_glu_grad, "w4a8_glu_grad", dh, dev, lambda: grad_workspace_size(m, k, n, 2, dh.dtype),
               (dh.data_ptr(), m, n, lddh, g.data_ptr(), u.data_ptr(), ldg, wg.data_ptr(), _vector(sg, "sg", n, dev),
                wu.data_ptr(), _vector(su, "su", n, dev), ldp, k, code, flags, dx.data_ptr(), lddx, _at(dbg),
-               _at(dbu)), workspace, stream)
+               _at(dbu)), workspace)
     return (dx, dbg, dbu) if bias_grad else dx
 
 
