@@ -13,6 +13,10 @@ class FakeStream:
     cuda_stream = 0x5EED
 
 
+class CallerStream:
+    cuda_stream = 0
+
+
 class FakeLib:
     """Every function succeeds; sizes are 64; calls and the current stream are recorded."""
 
@@ -49,7 +53,7 @@ def world(monkeypatch):
     lib = FakeLib(now)
     monkeypatch.setattr(native, "lib", lib)
     monkeypatch.setattr(torch.cuda, "stream", entered)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: FakeStream() if now[0] == "given" else object())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: FakeStream() if now[0] == "given" else CallerStream())
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream",
                         lambda dev: FakeStream.cuda_stream if now[0] == "given" else 0, raising=False)
@@ -67,7 +71,17 @@ MLP = {
     "w4a8_linear_act_grad": dict(dy=DY, wp=WP, sw=SW, k=8, bias_grad=True),
     "w4a8_glu_grad": dict(dh=DY, g=DY, u=DY, wg=WP, sg=SW, wu=WP, su=SW, k=8, bias_grad=True),
 }
-CALLS = MLP
+W, XQ, SX, ZP = torch.zeros(8, 4), torch.zeros(2, 16, dtype=torch.int8), torch.ones(2), torch.zeros(4, dtype=torch.int32)
+W8 = torch.zeros(4, 16, dtype=torch.int8)
+CALLS = dict(MLP,
+    w4_quantize_pack=dict(w=W), a8_quantize_rows=dict(x=X), w8_quantize=dict(w=W), w4z_quantize_pack=dict(w=W),
+    w4g_quantize_pack=dict(w=W),
+    w4a8_linear=dict(x=X, wp=WP, sw=SW), w4a8_linear_q=dict(xq=XQ, sx=SX, k=8, wp=WP, sw=SW),
+    w4a8_linear_chain=dict(x=X, wp=WP, sw=SW), w4a8_linear_noalloc=dict(x=X, wp=WP, sw=SW),
+    w4a8_linear_grouped=dict(problems=[(X, WP, SW, None), (X, WP, SW, SW)]),
+    w8a8_linear=dict(x=X, wq=W8, sw=SW), w8a8_linear_q=dict(xq=XQ, sx=SX, k=8, wq=W8, sw=SW),
+    w4z_linear=dict(x=X, wp=WP, sa=SW, zp=ZP), w4z_linear_q=dict(xq=XQ, sx=SX, k=8, wp=WP, sa=SW, zp=ZP),
+    w4g_linear=dict(x=X, wp=WP, sa=SW, zp=ZP), w4g_linear_q=dict(xq=XQ, sx=SX, k=8, wp=WP, sa=SW, zp=ZP))
 
 
 @pytest.mark.parametrize("name", CALLS)

@@ -167,6 +167,8 @@ def flags_for(relu: bool = False, out: str = "f32", path: str = "auto",
 def w4_quantize_pack(w: torch.Tensor, wp: torch.Tensor | None = None,
                      sw: torch.Tensor | None = None, stream=None):
     """W[K][N] float32 (CUDA) -> (Wp[N][ldp] uint8, sw[N] float32)."""
+    if stream is not None:
+        return _under(stream, w4_quantize_pack, locals())
     ldw = _rowmajor(w, "W")
     k, n = w.shape
     if wp is None:
@@ -174,7 +176,7 @@ def w4_quantize_pack(w: torch.Tensor, wp: torch.Tensor | None = None,
     if sw is None:
         sw = torch.empty(n, dtype=torch.float32, device=w.device)
     ldp = _rowmajor(wp, "Wp")
-    _check(lib.w4_quantize_pack(_ptr(w), k, n, ldw, _ptr(wp), ldp, _ptr(sw), _stream(stream)),
+    _check(lib.w4_quantize_pack(_ptr(w), k, n, ldw, _ptr(wp), ldp, _ptr(sw), _stream()),
            "w4_quantize_pack")
     return wp, sw
 
@@ -182,6 +184,8 @@ def w4_quantize_pack(w: torch.Tensor, wp: torch.Tensor | None = None,
 def a8_quantize_rows(x: torch.Tensor, xq: torch.Tensor | None = None,
                      sx: torch.Tensor | None = None, stream=None):
     """X[M][K] float32 (CUDA) -> (Xq[M][ldq] int8, sx[M] float32)."""
+    if stream is not None:
+        return _under(stream, a8_quantize_rows, locals())
     ldx = _rowmajor(x, "X")
     m, k = x.shape
     if xq is None:
@@ -189,7 +193,7 @@ def a8_quantize_rows(x: torch.Tensor, xq: torch.Tensor | None = None,
     if sx is None:
         sx = torch.empty(m, dtype=torch.float32, device=x.device)
     ldq = _rowmajor(xq, "Xq")
-    _check(lib.a8_quantize_rows(_ptr(x), m, k, ldx, _ptr(xq), ldq, _ptr(sx), _stream(stream)),
+    _check(lib.a8_quantize_rows(_ptr(x), m, k, ldx, _ptr(xq), ldq, _ptr(sx), _stream()),
            "a8_quantize_rows")
     return xq, sx
 
@@ -209,6 +213,8 @@ def w4a8_linear(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor,
 
     static_weights: promise that wp, sw and bias are final and not written by
     work still pending on the stream (W4A8_STATIC_WEIGHTS)."""
+    if stream is not None:
+        return _under(stream, w4a8_linear, locals())
     ldx = _rowmajor(x, "X")
     ldp = _rowmajor(wp, "Wp")
     m, k = x.shape
@@ -219,7 +225,7 @@ def w4a8_linear(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor,
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
     _check(lib.w4a8_linear(_ptr(x), m, k, ldx, _ptr(wp), ldp, _ptr(sw), n, _ptr(bias),
                            flags_for(relu, out, path, static_weights), _ptr(y), ldy, _ptr(workspace),
-                           workspace.numel() * workspace.element_size(), _stream(stream)),
+                           workspace.numel() * workspace.element_size(), _stream()),
            "w4a8_linear")
     return y
 
@@ -229,6 +235,8 @@ def w4a8_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor,
                   out: str = "f32", path: str = "auto", y: torch.Tensor | None = None,
                   stream=None, static_weights: bool = False) -> torch.Tensor:
     """Y from INT8 activations Xq[M][ldq] (first k bytes of each row) and sx[M]."""
+    if stream is not None:
+        return _under(stream, w4a8_linear_q, locals())
     ldq = _rowmajor(xq, "Xq")
     ldp = _rowmajor(wp, "Wp")
     m = xq.shape[0]
@@ -236,7 +244,7 @@ def w4a8_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor,
     y, ldy = _out_tensor(y, m, n, out, xq.device)
     _check(lib.w4a8_linear_q(_ptr(xq), m, k, ldq, _ptr(sx), _ptr(wp), ldp, _ptr(sw), n,
                              _ptr(bias), flags_for(relu, out, path, static_weights), _ptr(y), ldy,
-                             _stream(stream)),
+                             _stream()),
            "w4a8_linear_q")
     return y
 
@@ -254,6 +262,8 @@ def w4a8_linear_chain(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor,
     """One chained Dense layer: Y[M][N] float32 as w4a8_linear, taking the
     input's per-row abs-max parts x_amax [M][parts] (or None) and returning
     (Y, y_amax) with y_amax [M][amax_parts(N)] (None if emit_amax is False)."""
+    if stream is not None:
+        return _under(stream, w4a8_linear_chain, locals())
     ldx = _rowmajor(x, "X")
     ldp = _rowmajor(wp, "Wp")
     m, k = x.shape
@@ -274,7 +284,7 @@ def w4a8_linear_chain(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor,
     _check(lib.w4a8_linear_chain(_ptr(x), m, k, ldx, _ptr(x_amax), x_parts, _ptr(wp), ldp, _ptr(sw), n,
                                  _ptr(bias), flags_for(relu, "f32", path, static_weights), _ptr(y), ldy,
                                  _ptr(y_amax), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                 _stream(stream)),
+                                 _stream()),
            "w4a8_linear_chain")
     return y, y_amax
 
@@ -284,6 +294,8 @@ def w4a8_linear_grouped(problems, relu: bool = False, out: str = "f32", stream=N
     """Many independent few-row linears in as few launches as possible.
     problems: list of (x, wp, sw, bias_or_None) with x [M][K] float32, M <= 4.
     Returns the list of outputs Y [M][N]."""
+    if stream is not None:
+        return _under(stream, w4a8_linear_grouped, locals())
     arr = (Problem * max(1, len(problems)))()
     ys = []
     for i, (x, wp, sw, bias) in enumerate(problems):
@@ -296,7 +308,7 @@ def w4a8_linear_grouped(problems, relu: bool = False, out: str = "f32", stream=N
         arr[i] = Problem(x.data_ptr(), wp.data_ptr(), sw.data_ptr(), None if bias is None else bias.data_ptr(),
                          y.data_ptr(), m, k, ldx, ldp, n, ldy)
     flags = (RELU if relu else 0) | _OUT[out] | (STATIC_WEIGHTS if static_weights else 0)
-    _check(lib.w4a8_linear_grouped(arr, len(problems), flags, _stream(stream)), "w4a8_linear_grouped")
+    _check(lib.w4a8_linear_grouped(arr, len(problems), flags, _stream()), "w4a8_linear_grouped")
     return ys
 
 
@@ -310,6 +322,8 @@ def w4a8_linear_noalloc(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor,
                         stream=None, static_weights: bool = False) -> torch.Tensor:
     """w4a8_linear without a caller workspace: the INT8 activations live in the
     library's fixed per-device scratch array (see include/w4a8.h)."""
+    if stream is not None:
+        return _under(stream, w4a8_linear_noalloc, locals())
     ldx = _rowmajor(x, "X")
     ldp = _rowmajor(wp, "Wp")
     m, k = x.shape
@@ -317,7 +331,7 @@ def w4a8_linear_noalloc(x: torch.Tensor, wp: torch.Tensor, sw: torch.Tensor,
     y, ldy = _out_tensor(y, m, n, out, x.device)
     _check(lib.w4a8_linear_noalloc(_ptr(x), m, k, ldx, _ptr(wp), ldp, _ptr(sw), n, _ptr(bias),
                                    flags_for(relu, out, path, static_weights), _ptr(y), ldy,
-                                   _stream(stream)),
+                                   _stream()),
            "w4a8_linear_noalloc")
     return y
 
@@ -333,6 +347,8 @@ def w8a8_ld(k: int) -> int:
 def w8_quantize(w: torch.Tensor, wq: torch.Tensor | None = None,
                 sw: torch.Tensor | None = None, stream=None):
     """W[K][N] float32 (CUDA) -> (Wq[N][ldw8] int8, sw[N] float32)."""
+    if stream is not None:
+        return _under(stream, w8_quantize, locals())
     ldw = _rowmajor(w, "W")
     k, n = w.shape
     if wq is None:
@@ -340,7 +356,7 @@ def w8_quantize(w: torch.Tensor, wq: torch.Tensor | None = None,
     if sw is None:
         sw = torch.empty(n, dtype=torch.float32, device=w.device)
     ldw8 = _rowmajor(wq, "Wq")
-    _check(lib.w8_quantize(_ptr(w), k, n, ldw, _ptr(wq), ldw8, _ptr(sw), _stream(stream)), "w8_quantize")
+    _check(lib.w8_quantize(_ptr(w), k, n, ldw, _ptr(wq), ldw8, _ptr(sw), _stream()), "w8_quantize")
     return wq, sw
 
 
@@ -350,6 +366,8 @@ def w8a8_linear(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
                 workspace: torch.Tensor | None = None, stream=None,
                 static_weights: bool = False) -> torch.Tensor:
     """Y[M][N] = dequant(quant8(X) @ Wq^T) (+bias, ReLU) for X[M][K] float32."""
+    if stream is not None:
+        return _under(stream, w8a8_linear, locals())
     ldx = _rowmajor(x, "X")
     ldw8 = _rowmajor(wq, "Wq")
     m, k = x.shape
@@ -360,7 +378,7 @@ def w8a8_linear(x: torch.Tensor, wq: torch.Tensor, sw: torch.Tensor,
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
     _check(lib.w8a8_linear(_ptr(x), m, k, ldx, _ptr(wq), ldw8, _ptr(sw), n, _ptr(bias),
                            flags_for(relu, out, path, static_weights), _ptr(y), ldy, _ptr(workspace),
-                           workspace.numel() * workspace.element_size(), _stream(stream)),
+                           workspace.numel() * workspace.element_size(), _stream()),
            "w8a8_linear")
     return y
 
@@ -370,6 +388,8 @@ def w8a8_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wq: torch.Tensor,
                   out: str = "f32", path: str = "auto", y: torch.Tensor | None = None,
                   stream=None, static_weights: bool = False) -> torch.Tensor:
     """Y from INT8 activations Xq[M][ldq] (first k bytes of each row) and sx[M]."""
+    if stream is not None:
+        return _under(stream, w8a8_linear_q, locals())
     ldq = _rowmajor(xq, "Xq")
     ldw8 = _rowmajor(wq, "Wq")
     m = xq.shape[0]
@@ -377,7 +397,7 @@ def w8a8_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wq: torch.Tensor,
     y, ldy = _out_tensor(y, m, n, out, xq.device)
     _check(lib.w8a8_linear_q(_ptr(xq), m, k, ldq, _ptr(sx), _ptr(wq), ldw8, _ptr(sw), n,
                              _ptr(bias), flags_for(relu, out, path, static_weights), _ptr(y), ldy,
-                             _stream(stream)),
+                             _stream()),
            "w8a8_linear_q")
     return y
 
@@ -388,13 +408,15 @@ def w8a8_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wq: torch.Tensor,
 
 def w4z_quantize_pack(w: torch.Tensor, stream=None):
     """W[K][N] float32 (CUDA) -> (Wp[N][ldp] uint8, sa[N] float32, zp[N] int32)."""
+    if stream is not None:
+        return _under(stream, w4z_quantize_pack, locals())
     ldw = _rowmajor(w, "W")
     k, n = w.shape
     wp = torch.empty((n, packed_ld(k)), dtype=torch.uint8, device=w.device)
     sa = torch.empty(n, dtype=torch.float32, device=w.device)
     zp = torch.empty(n, dtype=torch.int32, device=w.device)
     _check(lib.w4z_quantize_pack(_ptr(w), k, n, ldw, _ptr(wp), wp.stride(0), _ptr(sa), _ptr(zp),
-                                 _stream(stream)), "w4z_quantize_pack")
+                                 _stream()), "w4z_quantize_pack")
     return wp, sa, zp
 
 
@@ -411,6 +433,8 @@ def w4z_linear(x: torch.Tensor, wp: torch.Tensor, sa: torch.Tensor, zp: torch.Te
                workspace: torch.Tensor | None = None, stream=None,
                static_weights: bool = False) -> torch.Tensor:
     """Y[M][N] of the zero-point layer for X[M][K] float32."""
+    if stream is not None:
+        return _under(stream, w4z_linear, locals())
     ldx = _rowmajor(x, "X")
     ldp = _rowmajor(wp, "Wp")
     m, k = x.shape
@@ -419,7 +443,7 @@ def w4z_linear(x: torch.Tensor, wp: torch.Tensor, sa: torch.Tensor, zp: torch.Te
     workspace, wsb = _zworkspace(workspace, m, k, n, x.device)
     _check(lib.w4z_linear(_ptr(x), m, k, ldx, _ptr(wp), ldp, _ptr(sa), _ptr(zp), n, _ptr(bias),
                           flags_for(relu, out, path, static_weights), _ptr(y), ldy, _ptr(workspace), wsb,
-                          _stream(stream)), "w4z_linear")
+                          _stream()), "w4z_linear")
     return y
 
 
@@ -429,6 +453,8 @@ def w4z_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor, s
                  workspace: torch.Tensor | None = None, stream=None,
                  static_weights: bool = False) -> torch.Tensor:
     """The zero-point layer on INT8 activations Xq[M][ldq] and sx[M]."""
+    if stream is not None:
+        return _under(stream, w4z_linear_q, locals())
     ldq = _rowmajor(xq, "Xq")
     ldp = _rowmajor(wp, "Wp")
     m = xq.shape[0]
@@ -437,7 +463,7 @@ def w4z_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor, s
     workspace, wsb = _zworkspace(workspace, m, k, n, xq.device)
     _check(lib.w4z_linear_q(_ptr(xq), m, k, ldq, _ptr(sx), _ptr(wp), ldp, _ptr(sa), _ptr(zp), n, _ptr(bias),
                             flags_for(relu, out, path, static_weights), _ptr(y), ldy, _ptr(workspace), wsb,
-                            _stream(stream)), "w4z_linear_q")
+                            _stream()), "w4z_linear_q")
     return y
 
 
@@ -446,6 +472,8 @@ def w4z_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor, s
 
 def w4g_quantize_pack(w: torch.Tensor, stream=None):
     """W[K][N] float32 (CUDA) -> (Wp[N][ldp] uint8, sa[N][ng] float32, zp[N][ng] int32)."""
+    if stream is not None:
+        return _under(stream, w4g_quantize_pack, locals())
     ldw = _rowmajor(w, "W")
     k, n = w.shape
     ng = lib.w4g_groups(k)
@@ -453,7 +481,7 @@ def w4g_quantize_pack(w: torch.Tensor, stream=None):
     sa = torch.empty((n, ng), dtype=torch.float32, device=w.device)
     zp = torch.empty((n, ng), dtype=torch.int32, device=w.device)
     _check(lib.w4g_quantize_pack(_ptr(w), k, n, ldw, _ptr(wp), wp.stride(0), _ptr(sa), _ptr(zp),
-                                 _stream(stream)), "w4g_quantize_pack")
+                                 _stream()), "w4g_quantize_pack")
     return wp, sa, zp
 
 
@@ -463,6 +491,8 @@ def w4g_linear(x: torch.Tensor, wp: torch.Tensor, sa: torch.Tensor, zp: torch.Te
                workspace: torch.Tensor | None = None, stream=None,
                static_weights: bool = False) -> torch.Tensor:
     """Y[M][N] of the group-wise layer for X[M][K] float32."""
+    if stream is not None:
+        return _under(stream, w4g_linear, locals())
     ldx = _rowmajor(x, "X")
     ldp = _rowmajor(wp, "Wp")
     m, k = x.shape
@@ -473,7 +503,7 @@ def w4g_linear(x: torch.Tensor, wp: torch.Tensor, sa: torch.Tensor, zp: torch.Te
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=x.device)
     _check(lib.w4g_linear(_ptr(x), m, k, ldx, _ptr(wp), ldp, _ptr(sa), _ptr(zp), n, _ptr(bias),
                           flags_for(relu, out, path, static_weights), _ptr(y), ldy, _ptr(workspace),
-                          workspace.numel() * workspace.element_size(), _stream(stream)), "w4g_linear")
+                          workspace.numel() * workspace.element_size(), _stream()), "w4g_linear")
     return y
 
 
@@ -482,13 +512,15 @@ def w4g_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor, s
                  out: str = "f32", path: str = "auto", y: torch.Tensor | None = None, stream=None,
                  static_weights: bool = False) -> torch.Tensor:
     """The group-wise layer on INT8 activations Xq[M][ldq] and sx[M]."""
+    if stream is not None:
+        return _under(stream, w4g_linear_q, locals())
     ldq = _rowmajor(xq, "Xq")
     ldp = _rowmajor(wp, "Wp")
     m = xq.shape[0]
     n = wp.shape[0]
     y, ldy = _out_tensor(y, m, n, out, xq.device)
     _check(lib.w4g_linear_q(_ptr(xq), m, k, ldq, _ptr(sx), _ptr(wp), ldp, _ptr(sa), _ptr(zp), n, _ptr(bias),
-                            flags_for(relu, out, path, static_weights), _ptr(y), ldy, _stream(stream)),
+                            flags_for(relu, out, path, static_weights), _ptr(y), ldy, _stream()),
            "w4g_linear_q")
     return y
 
