@@ -21,10 +21,13 @@ struct EpiArgs {
     int ldr, ldy, ldz;
 };
 
-// z = acc / (sx sw) + b as (acc (1/sx)) (1/sw) + b: no product of scales that
-// could overflow, the second product and the sum in one rounding.
+// z = acc / (sx sw) + b as acc ((1/sx) (1/sw)) + b, the product with acc and
+// the sum in one rounding. The reciprocals meet first: their product is what
+// one unit of acc weighs, so it overflows only where the result does. (With
+// acc / sx first, up to 2^31 times the row's abs-max, rows of 1e35 gave
+// infinities for results of 1e35.)
 __device__ __forceinline__ float dequant(float acc, float rsx, float rsw, float b) {
-    return __fmaf_rn(__fmul_rn(acc, rsx), rsw, b);
+    return __fmaf_rn(acc, __fmul_rn(rsx, rsw), b);
 }
 
 // One thread per output. The row is in the k-permuted order, so a packed word
