@@ -86,8 +86,20 @@ size_t forward_workspace(int M, int K, int N, bool glu) {
     return workspace_bytes_for(M, K, nullptr) + mlp::forward_plan(M, K, N, glu).part_bytes + 256;
 }
 
-// Few products: the CUDA-core form, whose launch is the cheapest.
+// Few products, and short sums: the CUDA-core forms, whose launch is the
+// cheapest. One thread walks a whole sum there, about 6.4 us per 1000 k and
+// 130 us per 1000 n of a gradient, so long ones go to the other forms.
+// Measured in a graph, CUDA cores against the decode (M <= 16) or tensor-core
+// form, float32. Forward: M 1, N 10: 2.4 / 2.5 us at K 128, 3.3 / 2.4 at K 256,
+// 27.5 / 3.2 at K 4096; M 4, N 4: 3.2 / 3.4 at K 256, 4.5 / 3.4 at K 512; M 8, N 4:
+// 4.6 / 5.1 at K 512, 7.2 / 5.1 at K 1024; M 20, N 4: 4.7 / 6.7 at K 512. Gradient,
+// M 1, K 10: 5.4 / 6.7 us at N 16, 7.7 / 6.5 at N 32, 842 / 18 at N 6500; M 128, K 2:
+// 5.7 / 8.3 at N 16, 7.8 / 8.3 at N 32, 11.9 / 8.3 at N 64.
 bool mlp_tiny(int M, int K, int N, int segs) { return (double)M * N * K * segs < 65536.0; }
+bool forward_tiny(int M, int K, int N, int segs) {
+    return mlp_tiny(M, K, N, segs) && K <= (M <= 2 ? 128 : M <= 4 ? 256 : 512);
+}
+bool grad_tiny(int M, int K, int N, int segs) { return mlp_tiny(M, K, N, segs) && segs * (long long)N <= 24; }
 
 template <bool GLU, typename T>
 w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a, const mlp::Proj &b, int ldp, int N,
@@ -97,9 +109,9 @@ w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a
     unsigned path = flags & W4A8_PATH_MASK;
     const mlp::DecPlan dec = mlp::dec_plan(M, K, N, GLU ? 8 : 16, sms);
     if (path == W4A8_PATH_AUTO)
-        path = mlp_tiny(M, K, N, GLU ? 2 : 1) ? W4A8_PATH_GENERIC
-               : dec.preferred                     ? W4A8_PATH_DECODE
-                                                   : W4A8_PATH_TC;
+        path = forward_tiny(M, K, N, GLU ? 2 : 1) ? W4A8_PATH_GENERIC
+               : dec.preferred                         ? W4A8_PATH_DECODE
+                                                       : W4A8_PATH_TC;
     if (path != W4A8_PATH_GENERIC && path != W4A8_PATH_DECODE && path != W4A8_PATH_TC) return W4A8_ERR_UNSUPPORTED;
     if (path == W4A8_PATH_DECODE && !dec.ok) return W4A8_ERR_UNSUPPORTED;
     if (path != W4A8_PATH_GENERIC && tc::encode_fn() == nullptr) return W4A8_ERR_UNSUPPORTED;
@@ -203,7 +215,7 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
     constexpr bool LO = std::is_same<T, float>::value;
     const int N = in.N;
     unsigned path = flags & W4A8_PATH_MASK;
-    if (path == W4A8_PATH_AUTO) path = mlp_tiny(M, K, N, SEGS) ? W4A8_PATH_GENERIC : W4A8_PATH_TC;
+    if (path == W4A8_PATH_AUTO) path = grad_tiny(M, K, N, SEGS) ? W4A8_PATH_GENERIC : W4A8_PATH_TC;
     if (path != W4A8_PATH_GENERIC && path != W4A8_PATH_TC) return W4A8_ERR_UNSUPPORTED;
     if (path == W4A8_PATH_TC && tc::encode_fn() == nullptr) return W4A8_ERR_UNSUPPORTED;
     unsigned launches = 0;
