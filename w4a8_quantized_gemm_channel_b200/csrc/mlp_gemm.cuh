@@ -1097,7 +1097,7 @@ inline PairPlan grad_plan(int M, int K, int segs, int seg, bool two) {
 // What a launch needs beside PairArgs: the operands' shapes.
 struct PairCall {
     const uint8_t *Wa, *Wb;
-    int w_rows, ldp;             // packed rows and their stride
+    int w_rows, k, ldp;          // packed rows, their codes and stride
     const void *X;               // INT8 rows [M][ldq], or FP16 rows [planes M][width]
     int x_rows, x_inner;         // rows and row elements (= stride) of X
 };
@@ -1113,9 +1113,11 @@ w4a8_status launch_pair(PairArgs p, const PairCall &c, cudaStream_t stream) {
     CUtensorMap wa, wb, x, out[3];
     memset(out, 0, sizeof(out));
     const uint32_t box_rows = S::FWD ? (GLU ? 64 : 128) : 64;
+    // A row's own bytes, not its stride: of the last row of a column range of a
+    // wider array the stride reaches past the array's end.
     auto map_w = [&](CUtensorMap *m, const uint8_t *W) {
-        return tc::make_map_u8(m, W, (uint64_t)c.ldp, (uint64_t)c.w_rows, (uint64_t)c.ldp, 64, box_rows,
-                               CU_TENSOR_MAP_SWIZZLE_64B);
+        return tc::make_map_u8(m, W, (uint64_t)packed_row_bytes(c.k), (uint64_t)c.w_rows, (uint64_t)c.ldp, 64,
+                               box_rows, CU_TENSOR_MAP_SWIZZLE_64B);
     };
     if (!map_w(&wa, c.Wa) || !map_w(&wb, c.Wb)) return W4A8_ERR_CUDA;
     const size_t xsz = S::FWD ? 1 : 2;
