@@ -2,6 +2,7 @@
 takes. Every call here is refused before its made-up addresses are used (the
 accepted sizes by a workspace that is too small)."""
 import pytest
+import torch
 
 from tests.test_mlp_abi import ARGS, GLU, GLU_GRAD, LIN, LIN_GRAD, call
 from w4a8_quantized_gemm_channel_b200 import native
@@ -43,3 +44,33 @@ def test_rejected_sizes_and_flags_need_no_workspace(m, k, n, flags):
     for projections in (1, 2):
         assert lib.w4a8_act_workspace_size(m, k, n, projections, flags) == 0
         assert lib.w4a8_grad_workspace_size(m, k, n, projections, flags) == 0
+
+
+class Rows:
+    """What the binding asks of a row tensor, without its memory."""
+    is_cuda = True
+
+    def __init__(self, shape, strides, dtype=torch.float32):
+        self.shape, self.strides, self.dtype = torch.Size(shape), strides, dtype
+
+    def dim(self):
+        return 2
+
+    def stride(self):
+        return self.strides
+
+    def get_device(self):
+        return 0
+
+
+def test_binding_passes_no_size_that_an_int_cuts_off():
+    big = 2 ** 32 + 8            # an int holds its low half, 8
+    assert native._rows_in(Rows((3, 8), (2 ** 31 - 1, 1)), "X") == (3, 8, 2 ** 31 - 1, 0)
+    for t in (Rows((3, 8), (big, 1)), Rows((big, 8), (8, 1)), Rows((3, big), (big, 1)), Rows((1, big), (big, 1))):
+        with pytest.raises(ValueError, match="fit an int"):
+            native._rows_in(t, "X")
+    assert native._rows_in(Rows((1, 8), (big, 1)), "X") == (1, 8, 8, 0)      # one row: its stride means nothing
+    for t, k in ((Rows((big, 16), (16, 1), torch.uint8), 8), (Rows((4, big), (big, 1), torch.uint8), 8),
+                 (Rows((4, big), (big, 1), torch.uint8), big)):
+        with pytest.raises(ValueError, match="fit an int"):
+            native._codes(t, "wp", k, 0)

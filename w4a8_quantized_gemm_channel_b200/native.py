@@ -534,7 +534,9 @@ def w4g_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor, s
 # stream, and what it reads must be ready there.
 
 # A call on few rows takes the GPU about as long as its marshalling takes the
-# host, so this part keeps to plain integers and checks each fact once.
+# host, so this part keeps to plain integers and checks each fact once. Sizes
+# are checked against _INT_MAX because ctypes cuts larger ones off silently.
+_INT_MAX = 2 ** 31 - 1
 
 def _mlp_flags(rows: torch.Tensor, act: str, path: str, static_weights: bool):
     """(flags, activation code) of a call on rows of this type."""
@@ -551,7 +553,11 @@ def _row_stride(t: torch.Tensor, name: str, rows: int, cols: int) -> int:
     ld, one = t.stride()
     if one != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return ld if rows > 1 else max(ld, cols)
+    if rows <= 1:
+        return max(ld, cols) if ld <= _INT_MAX else cols
+    if ld > _INT_MAX:
+        raise ValueError(f"{name}'s row stride of {ld} elements does not fit an int")
+    return ld
 
 
 def _rows_in(t: torch.Tensor, name: str):
@@ -559,6 +565,8 @@ def _rows_in(t: torch.Tensor, name: str):
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     m, n = t.shape
+    if m > _INT_MAX or n > _INT_MAX:
+        raise ValueError(f"{name} of shape {tuple(t.shape)}: sizes must fit an int")
     return m, n, _row_stride(t, name, m, n), t.get_device()
 
 
@@ -576,6 +584,8 @@ def _codes(wp: torch.Tensor, name: str, k: int, dev: int):
     if wp.dtype != torch.uint8 or wp.get_device() != dev or wp.dim() != 2 or wp.shape[1] < (k + 1) // 2:
         raise ValueError(f"{name} must be [N][>= {packed_ld(k)}] packed uint8 codes for K = {k} on device {dev}")
     n, cols = wp.shape
+    if n > _INT_MAX or k > _INT_MAX:
+        raise ValueError(f"{name}: N = {n}, K = {k} must fit an int")
     return n, _row_stride(wp, name, n, cols)
 
 
