@@ -74,3 +74,12 @@ def test_binding_passes_no_size_that_an_int_cuts_off():
                  (Rows((4, big), (big, 1), torch.uint8), big)):
         with pytest.raises(ValueError, match="fit an int"):
             native._codes(t, "wp", k, 0)
+
+
+def test_single_saved_rows_have_no_stride():
+    a, b = torch.zeros(2, 48)[:, :40], torch.zeros(2, 64)[:, :40]
+    assert native._saved(a[:1], b[:1], a, -1, 1, 40) == 40
+    assert native._saved(a, a, a, -1, 2, 40) == 48 and native._saved(None, None, a, -1, 2, 40) == 0
+    for g, u, m in ((a, b, 2), (a[:1], None, 1), (None, b, 2), (a[:0], None, 0)):
+        with pytest.raises(ValueError, match="one row stride"):
+            native._saved(g, u, a, -1, m, 40)

@@ -27,3 +27,24 @@ def test_weights_side_by_side(io, m, k, n):
         ref.check(native.w4a8_linear_act(x, vu, su, path=path), *ref.linear(x, qu, su, None, "none", None)[0], path)
         want, _ = ref.glu_grad(dh, g, u, qg, sg, qu, su, "silu", True)
         ref.check(native.w4a8_glu_grad(dh, g, u, vg, sg, vu, su, k, path=path), *want, f"dx {path}")
+
+
+def test_saved_rows_of_different_buffers():
+    """One row has no stride: G and U may be rows of unlike buffers. Several
+    rows need one stride."""
+    rnd, k, n = gen(5), 64, 40
+    (qg, sg, wg), (qu, su, wu) = weights(rnd, n, k), weights(rnd, n, k)
+    g, u = torch.zeros(3, 48, device="cuda")[:, :n], torch.zeros(3, 65, device="cuda")[:, 1:n + 1]
+    x, dh = rnd(1, k), rnd(1, n)
+    h, g1, u1 = native.w4a8_glu(x, wg, sg, wu, su, g=g[:1], u=u[:1])
+    for t, (w, e), what in zip((h, g1, u1), ref.glu(x, qg, sg, qu, su, None, None, "silu"), "hgu"):
+        ref.check(t, w, e, what)
+    assert (g[1:] == 0).all() and (u[1:] == 0).all()
+    want, _ = ref.glu_grad(dh, g1, u1, qg, sg, qu, su, "silu", True)
+    ref.check(native.w4a8_glu_grad(dh, g1, u1, wg, sg, wu, su, k), *want, "dx")
+    with pytest.raises(ValueError, match="one row stride"):
+        native.w4a8_glu(rnd(3, k), wg, sg, wu, su, g=g, u=u)
+    with pytest.raises(ValueError, match="one row stride"):
+        native.w4a8_glu(x, wg, sg, wu, su, g=g[:1])
+    with pytest.raises(ValueError, match="one row stride"):
+        native.w4a8_glu_grad(rnd(3, n), g, u, wg, sg, wu, su, k)

@@ -579,6 +579,17 @@ def _like(t: torch.Tensor | None, name: str, x: torch.Tensor, dev: int, m: int, 
     return _row_stride(t, name, m, n)
 
 
+def _saved(g: torch.Tensor | None, u: torch.Tensor | None, x: torch.Tensor, dev: int, m: int, n: int) -> int:
+    """Row stride of the gated form's saved pre-activations (0 for None); of
+    single rows it may differ."""
+    ldg, ldu = _like(g, "G", x, dev, m, n), _like(u, "U", x, dev, m, n)
+    if ldg != ldu:
+        if m > 1 or g is None or u is None:
+            raise ValueError("G and U must both be given, with one row stride")
+        return n
+    return ldg
+
+
 def _codes(wp: torch.Tensor, name: str, k: int, dev: int):
     """(N, row stride) of packed codes [N][>= ceil(k / 2)]."""
     if wp.dtype != torch.uint8 or wp.get_device() != dev or wp.dim() != 2 or wp.shape[1] < (k + 1) // 2:
@@ -669,9 +680,7 @@ def w4a8_glu(x: torch.Tensor, wg: torch.Tensor, sg: torch.Tensor, wu: torch.Tens
     h, ldh = (x.new_empty((m, n)), n) if h is None else (h, _like(h, "H", x, dev, m, n))
     if save and g is None and u is None:
         g, u = x.new_empty((m, n)), x.new_empty((m, n))
-    ldg, ldu = _like(g, "G", x, dev, m, n), _like(u, "U", x, dev, m, n)
-    if ldg != ldu:
-        raise ValueError("G and U must both be given, with one row stride")
+    ldg = _saved(g, u, x, dev, m, n)
     _mlp_call(lib.w4a8_glu, "w4a8_glu", x, dev, lambda: act_workspace_size(m, k, n, 2, x.dtype),
               (x.data_ptr(), m, k, ldx, wg.data_ptr(), _vector(sg, "sg", n, dev), wu.data_ptr(),
                _vector(su, "su", n, dev), ldp, n, _vector(gate_bias, "gate_bias", n, dev),
@@ -720,9 +729,9 @@ def w4a8_glu_grad(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, wg: torch.
     if rows != n:
         raise ValueError(f"dH must have {rows} columns")
     dx, lddx = (dh.new_empty((m, k)), k) if dx is None else (dx, _like(dx, "dX", dh, dev, m, k))
-    ldg, ldu = _like(g, "G", dh, dev, m, n), _like(u, "U", dh, dev, m, n)
-    if ldg != ldu or g is None:
+    if g is None:
         raise ValueError("G and U must both be given, with one row stride")
+    ldg = _saved(g, u, dh, dev, m, n)
     dbg, dbu = (torch.empty(n, dtype=torch.float32, device=dh.device) if bias_grad else None for _ in range(2))
     _mlp_call(lib.w4a8_glu_grad, "w4a8_glu_grad", dh, dev, lambda: grad_workspace_size(m, k, n, 2, dh.dtype),
               (dh.data_ptr(), m, n, lddh, g.data_ptr(), u.data_ptr(), ldg, wg.data_ptr(), _vector(sg, "sg", n, dev),
