@@ -304,18 +304,19 @@ __device__ __forceinline__ void load_pieces(uint4 (&v)[pieces<MODE>() * (WHOLE ?
     }
 }
 
-// Gives a packed slot back once this warp's loads of v have returned: lane 0
-// stores a value that depends on each of them before it arrives. (An mbarrier
-// arrive does not wait for loads in flight; behind loads that were merely
-// issued it let the slot be refilled under them.)
+// Gives a packed slot back once this warp's loads of v have returned: every
+// lane votes on a value that depends on each of its loads, and lane 0 stores
+// the outcome before it arrives. (An mbarrier arrive does not wait for loads
+// in flight; behind loads that were merely issued it let the slot be refilled
+// under them.)
 template <int N>
 __device__ __forceinline__ void give_back(uint64_t *bar, uint32_t *sink, const uint4 (&v)[N], int lane) {
     uint32_t d = v[0].x;
 #pragma unroll
     for (int i = 1; i < N; ++i) d ^= v[i].x;
-    __syncwarp();
+    const uint32_t all = __ballot_sync(0xffffffffu, d & 1u);
     if (lane == 0) {
-        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(ptx::smem_addr(sink)), "r"(d) : "memory");
+        asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(ptx::smem_addr(sink)), "r"(all) : "memory");
         ptx::mbar_arrive(bar);
     }
 }
