@@ -135,7 +135,7 @@ w4a8_status mlp_forward(const void *X, int M, int K, int ldx, const mlp::Proj &a
     if (path == W4A8_PATH_TC) {
         const int stages = (K + 255) / 256;
         const mlp::PairPlan plan = mlp::forward_plan(M, K, N, GLU);
-        const mlp::PairArgs p = {M, N, K, stages, stages, ws.sx, a, b, ea, act, 0, 1, nullptr};
+        const mlp::PairArgs p = {M, N, K, stages, stages, ws.sx, a, b, ea, act, 0, nullptr};
         const mlp::PairCall c = {a.Wp, b.Wp, N, K, ldp, ws.xq, M, ws.ldq};
         st = by_act(act, [&](auto A) {
             return mlp::launch_pair_any<GLU ? mlp::FWD_GLU : mlp::FWD_LINEAR, decltype(A)::value, T>(
@@ -245,9 +245,8 @@ w4a8_status mlp_grad(const mlp::GradIn<GLU, T> &in, int M, const uint8_t *Wa, co
     if (st != W4A8_OK) return st;
     if (path == W4A8_PATH_TC) {
         const int seg_stages = ws.seg / (LO ? 64 : 128);
-        // (the row pass lets dependents start only once all earlier work is done: the weights are settled)
         const mlp::PairArgs p = {M, K, N, seg_stages, SEGS * seg_stages, ws.rs, {}, {},
-                                 {nullptr, dX, nullptr, nullptr, 0, lddx, 0}, 0, 0, 1, nullptr};
+                                 {nullptr, dX, nullptr, nullptr, 0, lddx, 0}, 0, 0, nullptr};
         const mlp::PairCall c = {Wa, Wb, N, K, ldp, ws.P, ws.planes * M, SEGS * ws.seg};
         st = mlp::launch_pair_any<LO ? mlp::BWD_TWO : mlp::BWD_ONE, W4A8_ACT_NONE, T>(ws.plan, p, c, ws.tiles, s);
         if (st != W4A8_OK) return st;

@@ -145,7 +145,7 @@ struct PairArgs {
     const float *tok;   // sx, or the rows' powers of two
     Proj a, b;
     EpiArgs e;          // gradient: Y = dX
-    int act, tma_out, static_w;
+    int act, tma_out;
     uint32_t *parts;    // split calls: accumulators of partial tiles, else null
 };
 
@@ -584,9 +584,10 @@ k_mlp_pair(const __grid_constant__ CUtensorMap tm_wa, const __grid_constant__ CU
             }
         }
     };
-    // Static weights: the first stages' packed tiles are requested before the
-    // dependency wait; the tokens are read only after it.
-    const int pre_w = p.static_w ? min(S::P_SLOTS, total) : 0;
+    // The first stages' packed tiles are requested before the dependency wait:
+    // the row pass before this kernel lets it start only once all earlier work
+    // is done, so the weights are settled. The tokens are read after the wait.
+    const int pre_w = min(S::P_SLOTS, total);
     if (warp == 0 && lane == 0) {
         Run r = run0;
         for (int it = 0, st = r.s0; it < pre_w; ++it) {
