@@ -436,7 +436,8 @@ W4A8_API w4a8_status w4g_linear_q(const int8_t *Xq, int M, int K, int ldq, const
  * finite. A bfloat16 output is rounded once, from float32. In the gradients
  * each dz / sw is rounded to FP16 relative to a power of two of its row
  * (2^-11 of the value) for bfloat16 rows, and held in two FP16 terms (2^-22)
- * for float32 rows; sums are float32. Every call repeats bit for bit.
+ * for float32 rows, in either case no finer than 2^-39 of the row's largest;
+ * sums are float32. Every call repeats bit for bit.
  *
  * 1 <= K <= W4A8_ACT_MAX_K; M and N below 2^30, N of w4a8_glu_grad at most
  * 2^30 - 128. flags: W4A8_IO_* | W4A8_STATIC_WEIGHTS | one W4A8_PATH_*: AUTO

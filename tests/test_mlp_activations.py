@@ -2,7 +2,9 @@
 
 A zero row makes the pre-activation the bias itself, and one row of gradients
 makes the bias gradient the derivative itself, so the calls give act(z),
-act'(z) and the backward pass's own act(z) for any float32 z.
+act'(z) and the backward pass's own act(z) for any float32 z. (mlp_reference
+derives its bounds for activations from other functions; the first test here
+shows that they hold for these.)
 
 Bounds from the kernel's arithmetic (U = 2^-24, first order). ex2.approx: 4 U
 relative; rcp.approx: 2 U; every other float32 operation and constant: U.

@@ -39,7 +39,7 @@ __device__ __forceinline__ float gelu_tanh_arg(float z) {
 
 // e = exp(-z^2 / 2) and Phi(-|z|) = e g(|z|): g(x) = erfcx(x / sqrt(2)) / 2 is
 // smooth in t = 1 / (1 + 0.3 x), here the polynomial of degree 8 in t with the
-// least relative error over 0 <= x <= 14 (5.8e-8; 7 ulp evaluated in float32),
+// least relative error over 0 <= x <= 14 (5.8e-8; 7 2^-24 evaluated in float32),
 // found by reweighted least squares against float64 erfcx. The tail keeps its
 // relative accuracy, so z Phi(z) has no cancellation for negative z.
 __device__ __forceinline__ float normal_tail(float z, float &e) {
@@ -229,9 +229,11 @@ struct Raw8 {
 // exactly), codes stored in the k-permuted order of the nibble unpack (k0 k2
 // k4 k6 k1 k3 k5 k7 in every 8), the bytes from K to ldq zero. Bound: reading X.
 //
-// One block per row, the row's bytes kept as loaded between the two steps (a
-// row that does not fit is read twice): few registers, so many blocks per SM
-// whose loads, reductions and stores overlap.
+// One block per row, the row's bytes kept as loaded between the two steps: few
+// registers, so many blocks per SM whose loads, reductions and stores overlap.
+// Rows of up to 8 THREADS UNITS values fit (12288 in the widest form); longer
+// ones are read twice. A bfloat16 call of 2048 rows and 256 channels takes 36.6
+// us at K = 12288, 51.1 at 12304, 84.8 at 28672.
 template <typename T, int THREADS, int UNITS>
 __global__ void __launch_bounds__(THREADS)
 k_quant_rows(const T *X, int M, int K, int ldx, int8_t *__restrict__ Xq, int ldq, float *__restrict__ sx,
@@ -466,7 +468,8 @@ k_grad_rows(GradIn<GLU, T> in, int M, int seg, __half *__restrict__ P, float *__
 // slice writes the result; more leave partial sums that k_bias_grad_sum adds
 // in order. Sums are float32 over at most BG_ROWS / 64 rows, then 64, then the
 // slices. Bound: HBM, the rows read once more; at few rows the launch, hence
-// one where one slice covers them.
+// one where one slice covers them. Beside a gradient of 2048 x 4096 x 11008
+// (M, K, N) in bfloat16 it adds 35 us (GELU), gated 50 us (SiLU).
 constexpr int BG_ROWS = 256, BG_COLS = 64, BG_GROUPS = 64;
 
 template <bool GLU, int ACT, typename T>

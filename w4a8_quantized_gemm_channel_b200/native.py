@@ -531,7 +531,8 @@ def w4g_linear_q(xq: torch.Tensor, sx: torch.Tensor, k: int, wp: torch.Tensor, s
 # float32 or all bfloat16; act is "none", "relu", "silu", "gelu" or
 # "gelu_tanh". Formulas and rules: include/w4a8.h. A call runs on `stream`, the
 # current one by default; outputs and workspace that it allocates belong to that
-# stream, and what it reads must be ready there.
+# stream, and what it reads must be ready there. The calls take and return plain
+# values: autograd does not record them, the gradient calls are made by hand.
 
 # A call on few rows takes the GPU about as long as its marshalling takes the
 # host, so this part keeps to plain integers and checks each fact once. Sizes
